@@ -353,6 +353,159 @@ zdec_status zdec_q4k_gemm(const void *repacked_dev, int N, int K, const float *x
 zdec_status zdec_q4k_gemm_static(const void *repacked_dev, int N, int K, const float *x_dev, int B,
                                  float *y_dev, int impl, void *stream);
 
+/* ------------------------------------------------ chunks of new tokens ---
+ * Several new tokens per sequence into and over a paged cache: prompt chunks,
+ * prompts mixed with single tokens, queries over another stream's cached
+ * states.  The pages describe the decode step and a paged cache only; these
+ * four operators are what stands before it ("Eight concurrent agents pull
+ * 5.6x more tokens from one RX 9070 XT", section "What I am building next":
+ * sequences admitted into slots of a paged KV manager).  They keep no state:
+ * a cache is a zdec_pool, a caller's own device memory or a context's
+ * (zdec_get_cache).
+ *   zdec_chunk_plan        offsets, positions, pages and slots of a ragged batch
+ *   zdec_chunk_append      rotary embedding, encoding, scatter into the pages
+ *   zdec_chunk_read        cached tokens back as dense fp16 rows
+ *   zdec_chunk_attention   attention of the new tokens over their pages
+ * A batch of R requests holds its new tokens packed: request r has tokens
+ * cu[r] .. cu[r+1]-1.  A token's slot is page * 64 + (its position mod 64),
+ * int64, -1 for a token without one.  Block tables are [R][max_pages] int32:
+ * the page of each 64 tokens of a request's sequence.
+ * head_dim is 128.  All calls are asynchronous on `stream` (NULL: the legacy
+ * default stream) of the current device, which owns every dev pointer; they
+ * allocate nothing and may be captured into a CUDA graph, which replays with
+ * the values that the device arrays hold then. */
+typedef enum { ZDEC_F32 = 0, ZDEC_F16 = 1, ZDEC_BF16 = 2 } zdec_float_type;
+
+/* A pool of KV pages in device memory: n_pages pages of zdec_page_bytes bytes
+ * each, a page holding 64 tokens of one sequence for every layer and kv head
+ * (layer-major; per (layer, kv head) the K region, then the V region, in the
+ * layout that zdec_append_kv and the decode step use). */
+typedef struct {
+    void *base;              /* dev, 16-byte aligned                             */
+    int n_pages;             /* 1 .. 2^30                                        */
+    int n_layers, n_kv_heads;
+    int k_type, v_type;      /* zdec_kv_dtype of K and V                         */
+} zdec_pool;
+/* Bytes of one page (0 for a bad type or shape). */
+size_t zdec_page_bytes(int k_type, int v_type, int n_layers, int n_kv_heads);
+
+/* The cache of a context as the chunk operators take it: its pool, its block
+ * tables [max_slots][max_pages] and device lengths [max_slots] (read only for
+ * the caller), and the stream its calls run on.  Valid until zdec_destroy. */
+typedef struct {
+    zdec_pool pool;
+    const int32_t *tables;   /* dev */
+    const int32_t *lengths;  /* dev */
+    int max_slots, max_pages;
+    void *stream;
+} zdec_cache_view;
+zdec_status zdec_get_cache(const zdec_ctx *ctx, zdec_cache_view *view);
+/* Extend slots[i] (n distinct slots, host array) by n_new[i] >= 0 tokens:
+ * takes their pool pages, updates the block tables and advances the lengths,
+ * as zdec_append_kv does, but writes no K/V: the caller writes the new tokens
+ * of every layer (zdec_chunk_append) before anything reads them, on the
+ * context's stream or ordered with it.  Waits for the stream.
+ * ZDEC_ERR_CAPACITY if a slot would exceed max_L or the pool lacks pages
+ * (then nothing has changed). */
+zdec_status zdec_extend(zdec_ctx *ctx, int n, const int32_t *slots, const int32_t *n_new);
+
+/* Bits that the device sets in the optional status word (dev uint32, OR-ed,
+ * never cleared by these calls). */
+enum { ZDEC_CHUNK_BAD_SLOT = 1,   /* append, read: a slot past the pool (its row was skipped / read as 0)  */
+       ZDEC_CHUNK_NO_PAGE = 2,    /* attention: a key without a page in the pool (it was left out)         */
+       ZDEC_CHUNK_TIMEOUT = 4 };  /* attention: a bounded device wait gave up (outputs are not valid)      */
+
+/* The plan of a ragged batch, from its lengths on the device:
+ *   cu[r] = sum of n_new[0..r-1], cu[R] the total; kv_len[r] = ctx_len[r] + n_new[r];
+ *   token cu[r] + i has position ctx_len[r] + i.
+ * Table row r holds the pages of the ctx_len[r] cached tokens in its first
+ * ceil(ctx_len[r] / 64) entries.  With free_pages, the entries that the new
+ * tokens need behind those are set: page numbers free_pages[0], [1], ... in
+ * order of requests and positions.  Without (NULL) the table is only read.
+ * slots[t]: the token's slot, -1 where its table entry is negative, the free
+ * list is too short or its position is past the table (64 * max_pages).
+ * taken[0] = pages needed (above n_free: the last of them were not there and
+ * their entries are -1), taken[1] = cu[R].  Tokens cu[R] .. T-1 get position
+ * and slot -1; tokens past T are not written (nor the table entries that they
+ * would set).  A negative length counts as 0.  Lengths and the total stay
+ * below 2^31.  Two calls that set entries of the same table must be ordered.
+ * cu [R+1], kv_len [R], positions [T], slots [T], taken [2]. 0 <= R <= 2^20,
+ * 0 <= T < 2^31. */
+zdec_status zdec_chunk_plan(int R, const int32_t *ctx_len_dev, const int32_t *n_new_dev,
+                            const int32_t *free_pages_dev, int n_free, int32_t *tables_dev, int max_pages,
+                            int T, int32_t *cu_dev, int32_t *kv_len_dev, int32_t *positions_dev,
+                            int64_t *slots_dev, int32_t *taken_dev, void *stream);
+
+/* Rotary embedding of rotate-half pairs (i, i + 64), i = 0..63: pair i turns by
+ * position[axis(i)] * theta^(-i/64).  One axis for text; several (time,
+ * height, width) for images and video, the first sections[0] pairs taking
+ * axis 0, the next sections[1] axis 1, ...; the sections sum to 64. */
+typedef struct {
+    float theta;         /* > 0; 0: no rotation                                */
+    int axes;            /* 1 .. 4                                             */
+    int sections[4];     /* pairs of each axis                                 */
+} zdec_rope;
+
+/* Append T tokens to layer `layer` of the cache.  qkv_dev: rows of n_q query,
+ * n_kv key and n_kv value heads of 128 (type in_type, qkv_ld elements from row
+ * to row, a multiple of 8; 16-byte aligned).  positions_dev [axes][T] int32.
+ * Queries and keys are rotated in fp32 (angles reduced in 64-bit fixed point);
+ * rotated queries go to q_out_dev (q_type ZDEC_F16 or ZDEC_BF16, rows q_ld
+ * elements apart, a multiple of 8, 16-byte aligned; NULL with n_q = 0: none),
+ * keys and values are rounded to fp16 and encoded by their cache types (the
+ * rules of zdec_kv_dtype) at slots_dev[t].  A token with slot -1 (any negative
+ * value) writes no K/V, its query is still rotated.  Slots are distinct: of
+ * two tokens with one slot, either may be there afterwards, element by
+ * element.  status_dev: optional device word (NULL: none). */
+zdec_status zdec_chunk_append(const zdec_pool *pool, int layer, const zdec_rope *rope, int T, int n_q,
+                              const void *qkv_dev, int in_type, long long qkv_ld,
+                              const int32_t *positions_dev, const int64_t *slots_dev,
+                              void *q_out_dev, int q_type, long long q_ld, uint32_t *status_dev, void *stream);
+
+/* K and V of T slots of layer `layer` as fp16 rows k_dev, v_dev
+ * [T][n_kv_heads][128] (16-byte aligned): fp16 as stored, FP8 exactly, Q8_0 as
+ * code * scale rounded to fp16; negative and out-of-range slots read as 0.
+ * status_dev as above. */
+zdec_status zdec_chunk_read(const zdec_pool *pool, int layer, int T, const int64_t *slots_dev,
+                            void *k_dev, void *v_dev, uint32_t *status_dev, void *stream);
+
+/* Attention of the new tokens of R requests over their pages:
+ *   o[t][h] = sum_j softmax_j(scale * q[t][h] . k[j][h / (n_q / n_kv)]) v[j][...]
+ * over the keys j < kv_len[r] (at most 64 * max_pages) that token t sees:
+ *   causal: j <= kv_len[r] - n + i for the i-th of the request's n tokens (the
+ *     new tokens are the last of the kv_len[r] cached ones; with kv_len < n
+ *     the first tokens see nothing), and with window > 0 only the last
+ *     `window` of those;
+ *   not causal: all (cross attention over cached states of another length).
+ * A token that sees no key gets 0.  Keys past kv_len and values that a token
+ * does not see have no influence, whatever they hold.  Keys without a page in
+ * the pool are left out (ZDEC_CHUNK_NO_PAGE).
+ * q_dev, o_dev: fp16 or bf16 (io_type) rows of n_q heads of 128, q_ld and o_ld
+ * elements apart (multiples of 8; 16-byte aligned; they may not overlap).
+ * cu_dev [R+1] with cu[0] = 0, not decreasing; tokens past T are left out and
+ * rows behind cu[R] are not touched.  tables_dev [R][max_pages].
+ * Scores, softmax statistics and sums are fp32; probabilities enter the
+ * second product as fp16, and so do Q8_0 values (code * scale).
+ * workspace_dev: zdec_chunk_attention_workspace_bytes(n_q, n_kv) bytes,
+ * 256-byte aligned, any content; calls that may overlap in time need their
+ * own (two captured graphs that replay together too). */
+typedef struct {
+    int n_q;                 /* query heads, a multiple of n_kv_heads, at most 64 times it */
+    int R;                   /* 0 .. 2^20                                                   */
+    int T;                   /* rows of q and o                                             */
+    int max_pages;           /* table entries per request                                   */
+    int io_type;             /* ZDEC_F16 or ZDEC_BF16                                       */
+    int causal;
+    int window;              /* 0: none; > 0 needs causal                                   */
+    float scale;             /* > 0                                                         */
+    long long q_ld, o_ld;
+} zdec_chunk_attn;
+size_t zdec_chunk_attention_workspace_bytes(int n_q, int n_kv_heads);
+zdec_status zdec_chunk_attention(const zdec_pool *pool, int layer, const zdec_chunk_attn *a,
+                                 const int32_t *cu_dev, const int32_t *kv_len_dev, const int32_t *tables_dev,
+                                 const void *q_dev, void *o_dev, void *workspace_dev, size_t workspace_bytes,
+                                 uint32_t *status_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,12 +17,16 @@ from . import _build
 
 __all__ = ["ModelDesc", "Decoder", "ZdecError", "load_library", "q4k_repacked_bytes",
            "q4k_repack", "q4k_gemm", "q4k_gemm_workspace_bytes", "q4k_gemm_static",
+           "KVPool", "page_bytes", "chunk_plan", "chunk_append", "chunk_read", "chunk_attention",
+           "chunk_attention_workspace_bytes", "CHUNK_BAD_SLOT", "CHUNK_NO_PAGE", "CHUNK_TIMEOUT",
            "Q4K_GEMM_STATIC_MAX_KB", "KV_F16", "KV_Q8_0", "KV_FP8", "PAGE_TOKENS",
            "KERNEL_KINDS", "T_EMBED", "T_WQ", "T_WK", "T_WV", "T_WO", "T_GATE", "T_UP", "T_DOWN"]
 
 KV_F16, KV_Q8_0, KV_FP8 = 0, 1, 2   # per-tensor cache types (zdec_kv_dtype)
 PAGE_TOKENS = 64                    # tokens per KV pool page
 Q4K_GEMM_STATIC_MAX_KB = 262144   # K*B limit of q4k_gemm_static (ZDEC_Q4K_GEMM_STATIC_MAX_KB)
+F32, F16, BF16 = 0, 1, 2            # element types of the chunk operators (zdec_float_type)
+CHUNK_BAD_SLOT, CHUNK_NO_PAGE, CHUNK_TIMEOUT = 1, 2, 4   # bits of their status word
 STEP_HOST_IO, STEP_EAGER = 1, 2
 T_EMBED, T_WQ, T_WK, T_WV, T_WO, T_GATE, T_UP, T_DOWN = range(8)
 KERNEL_KINDS = ["embed", "-", "gemm_qkv", "attention", "gemm_o", "gemm_gateup", "gemm_down",
@@ -37,7 +41,9 @@ EXPORTS = ["zdec_create_cache", "zdec_create", "zdec_destroy", "zdec_append_kv",
            "zdec_get_info", "zdec_profile_step", "zdec_debug_export_q4k", "zdec_debug_dequant",
            "zdec_debug_read_kv", "zdec_debug_block_table", "zdec_debug_capture_hidden",
            "zdec_debug_attention", "zdec_debug_set_wait_limit", "zdec_q4k_repacked_bytes", "zdec_q4k_repack",
-           "zdec_q4k_gemm_workspace_bytes", "zdec_q4k_gemm", "zdec_q4k_gemm_static"]
+           "zdec_q4k_gemm_workspace_bytes", "zdec_q4k_gemm", "zdec_q4k_gemm_static", "zdec_page_bytes",
+           "zdec_get_cache", "zdec_extend", "zdec_chunk_plan", "zdec_chunk_append", "zdec_chunk_read",
+           "zdec_chunk_attention", "zdec_chunk_attention_workspace_bytes"]
 
 
 class ZdecError(RuntimeError):
@@ -73,6 +79,26 @@ class _Info(ctypes.Structure):
                 ("matvec_max_B", ctypes.c_int), ("attn_segments", ctypes.c_int),
                 ("k_type", ctypes.c_int), ("v_type", ctypes.c_int), ("page_tokens", ctypes.c_int),
                 ("pool_pages", ctypes.c_int), ("free_pages", ctypes.c_int)]
+
+
+class _Pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("n_layers", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("k_type", ctypes.c_int), ("v_type", ctypes.c_int)]
+
+
+class _CacheView(ctypes.Structure):
+    _fields_ = [("pool", _Pool), ("tables", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("max_slots", ctypes.c_int), ("max_pages", ctypes.c_int), ("stream", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_float), ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4)]
+
+
+class _ChunkAttn(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int), ("R", ctypes.c_int), ("T", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("io_type", ctypes.c_int), ("causal", ctypes.c_int), ("window", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_ld", ctypes.c_longlong), ("o_ld", ctypes.c_longlong)]
 
 
 _lib = None
@@ -128,6 +154,19 @@ def load_library(build_if_missing: bool = True):
         "zdec_q4k_gemm": (i, [vp, i, i, vp, i, vp, i, vp, sz, vp]),
         "zdec_q4k_gemm_static": (i, [vp, i, i, vp, i, vp, i, vp]),
     }
+    ll = ctypes.c_longlong
+    sigs.update({
+        "zdec_page_bytes": (sz, [i, i, i, i]),
+        "zdec_get_cache": (i, [vp, ctypes.POINTER(_CacheView)]),
+        "zdec_extend": (i, [vp, i, vp, vp]),
+        "zdec_chunk_plan": (i, [i, vp, vp, vp, i, vp, i, i, vp, vp, vp, vp, vp, vp]),
+        "zdec_chunk_append": (i, [ctypes.POINTER(_Pool), i, ctypes.POINTER(_Rope), i, i, vp, i, ll, vp, vp, vp, i, ll,
+                                  vp, vp]),
+        "zdec_chunk_read": (i, [ctypes.POINTER(_Pool), i, i, vp, vp, vp, vp, vp]),
+        "zdec_chunk_attention_workspace_bytes": (sz, [i, i]),
+        "zdec_chunk_attention": (i, [ctypes.POINTER(_Pool), i, ctypes.POINTER(_ChunkAttn), vp, vp, vp, vp, vp, vp, sz,
+                                     vp, vp]),
+    })
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
         f.restype = res
@@ -326,6 +365,35 @@ class Decoder:
                                                _ptr(ids), _ptr(kind), _ptr(ms), cap, ctypes.byref(n)))
         return [(KERNEL_KINDS[kind[i]], float(ms[i])) for i in range(min(n.value, cap))]
 
+    # --------------------------------------------------------------- chunks
+    def cache(self) -> "KVPool":
+        """This decoder's own cache for the chunk operators: a KVPool whose
+        ``tables`` [max_B, max_L / 64] and ``lengths`` [max_B] are its block
+        tables and device lengths (int32 tensors, only to be read) and whose
+        ``stream`` is the stream the decoder's calls run on.  Keeps the
+        decoder alive; not valid after close()."""
+        view = _CacheView()
+        self._check(self.lib.zdec_get_cache(self.h, ctypes.byref(view)))
+        import torch
+        dev = torch.device("cuda", torch.cuda.current_device())
+        p = view.pool
+        nbytes = page_bytes((p.k_type, p.v_type), p.n_layers, p.n_kv_heads)
+        pages = _device_tensor(p.base, (p.n_pages, nbytes), "|u1", self, dev)
+        c = KVPool(pages, p.n_layers, p.n_kv_heads, (p.k_type, p.v_type))
+        c.tables = _device_tensor(view.tables, (view.max_slots, view.max_pages), "<i4", self, dev)
+        c.lengths = _device_tensor(view.lengths, (view.max_slots,), "<i4", self, dev)
+        c.stream = view.stream or 0
+        return c
+
+    def extend(self, slots, n_new):
+        """Take pages for n_new[i] more tokens of slots[i] and advance the
+        lengths; the caller writes their K/V in every layer (chunk_append)
+        before anything reads them.  Waits for the decoder's stream."""
+        sl, nn = np.ascontiguousarray(slots, np.int32), np.ascontiguousarray(n_new, np.int32)
+        if sl.ndim != 1 or sl.shape != nn.shape:
+            raise ZdecError(-1, "slots and n_new must be vectors of one length")
+        self._check(self.lib.zdec_extend(self.h, sl.size, _ptr(sl), _ptr(nn)))
+
     # ---------------------------------------------------------------- debug
     def set_wait_limit(self, cycles: int):
         """Bound of the projection kernels' stage waits in clock cycles (0: the
@@ -423,3 +491,174 @@ def q4k_gemm_static(repacked_dev, N: int, K: int, x_dev, y_dev, impl: int, strea
     B = x_dev.shape[0]
     _glob_check(load_library().zdec_q4k_gemm_static(_ptr(repacked_dev), N, K, _ptr(x_dev), B, _ptr(y_dev), impl,
                                                     ctypes.c_void_p(stream) if stream else None))
+
+
+# ------------------------------------------------- chunks of new tokens
+class _DeviceArray:
+    """Device memory that a decoder owns, as __cuda_array_interface__ (keeps the owner alive)."""
+
+    def __init__(self, ptr, shape, typestr, owner):
+        self.owner = owner
+        self.__cuda_array_interface__ = {"data": (ptr, False), "shape": shape, "typestr": typestr, "version": 3}
+
+
+def _device_tensor(ptr, shape, typestr, owner, dev):
+    import torch
+    return torch.as_tensor(_DeviceArray(ptr, shape, typestr, owner), device=dev)
+
+
+def page_bytes(kv_dtype, n_layers: int, n_kv_heads: int) -> int:
+    """Bytes of one 64-token page of a pool with these cache types (one, or a (K, V) pair)."""
+    kt, vt = (int(kv_dtype), int(kv_dtype)) if np.isscalar(kv_dtype) else (int(kv_dtype[0]), int(kv_dtype[1]))
+    return int(load_library().zdec_page_bytes(kt, vt, n_layers, n_kv_heads))
+
+
+class KVPool:
+    """A pool of KV pages as the chunk operators take it: ``pages`` is a
+    contiguous uint8 CUDA tensor [n_pages, page_bytes(...)] (zeros, or written
+    by chunk_append), kept by this object.  Decoder.cache() gives a decoder's
+    own pool."""
+
+    def __init__(self, pages, n_layers: int, n_kv_heads: int, kv_dtype=KV_F16):
+        kt, vt = (int(kv_dtype), int(kv_dtype)) if np.isscalar(kv_dtype) else (int(kv_dtype[0]), int(kv_dtype[1]))
+        nbytes = page_bytes((kt, vt), n_layers, n_kv_heads)
+        if nbytes == 0:
+            raise ZdecError(-1, "bad cache type or pool shape")
+        _tensor(pages, "pages", ("uint8",), (None, nbytes), None)
+        self.pages, self.n_layers, self.n_kv_heads, self.k_type, self.v_type = pages, n_layers, n_kv_heads, kt, vt
+        self.device = pages.device
+        self._c = _Pool(pages.data_ptr(), pages.shape[0], n_layers, n_kv_heads, kt, vt)
+        self._ref = ctypes.byref(self._c)
+
+
+_TYPE_ID = {"float32": F32, "float16": F16, "bfloat16": BF16}
+
+
+def _tensor(x, name, dtypes, shape, device, strided=False):
+    """Check a CUDA tensor's type, shape (None: any) and device; contiguous unless only its first stride is free."""
+    if not _is_cuda(x):
+        raise ZdecError(-1, f"{name} must be a CUDA tensor")
+    if str(x.dtype)[6:] not in dtypes:
+        raise ZdecError(-1, f"{name} must be {' or '.join(dtypes)}, not {str(x.dtype)[6:]}")
+    if x.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, x.shape)):
+        raise ZdecError(-1, f"{name} must have shape {shape}, not {tuple(x.shape)}")
+    if device is not None and x.device != device:
+        raise ZdecError(-1, f"{name} is on {x.device}, the rest on {device}")
+    if not (x[:1].is_contiguous() if strided else x.is_contiguous()):
+        raise ZdecError(-1, f"{name} must be contiguous" + (" within a row" if strided else ""))
+    return x
+
+
+def _call(device, stream, fn, *args):
+    """One stateless call on `device`, on `stream` (a cudaStream_t, or None: torch's current stream there)."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        s = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            s = fn(*args, stream)
+    _glob_check(s)
+
+
+def _opt(x, name, dtypes, shape, device):
+    return None if x is None else _tensor(x, name, dtypes, shape, device).data_ptr()
+
+
+def chunk_plan(ctx_len, n_new, tables, cu, kv_len, positions, slots, taken, free_pages=None, stream=None):
+    """Offsets, positions, pages and slots of a ragged batch of new tokens, from
+    its lengths on the device (zdec_chunk_plan).  int32 CUDA tensors ctx_len,
+    n_new [R], tables [R, max_pages] (entries of new pages are set when
+    free_pages is given), outputs cu [R + 1], kv_len [R], positions [T], taken
+    [2] and int64 slots [T].  Asynchronous."""
+    lib, dev, i32 = load_library(), getattr(ctx_len, "device", None), ("int32",)
+    _tensor(ctx_len, "ctx_len", i32, (None,), None)
+    R = ctx_len.shape[0]
+    _tensor(n_new, "n_new", i32, (R,), dev)
+    _tensor(tables, "tables", i32, (R, None), dev)
+    _tensor(cu, "cu", i32, (R + 1,), dev)
+    _tensor(kv_len, "kv_len", i32, (R,), dev)
+    _tensor(positions, "positions", i32, (None,), dev)
+    T = positions.shape[0]
+    _tensor(slots, "slots", ("int64",), (T,), dev)
+    _tensor(taken, "taken", i32, (2,), dev)
+    free = _opt(free_pages, "free_pages", i32, (None,), dev)
+    if free_pages is not None and free_pages.numel() == 0:
+        free = taken.data_ptr()   # an empty list: never read, but not "no list"
+    _call(dev, stream, lib.zdec_chunk_plan, R, ctx_len.data_ptr(), n_new.data_ptr(), free,
+          0 if free_pages is None else free_pages.numel(), tables.data_ptr(), tables.shape[1], T, cu.data_ptr(),
+          kv_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), taken.data_ptr())
+
+
+def chunk_append(cache: KVPool, layer: int, qkv, positions, slots, q_out=None, rope_theta: float = 1e6,
+                 sections=(64,), status=None, stream=None):
+    """Rotate the queries and keys of T new tokens, write the queries to q_out
+    and the keys and values, encoded, to the tokens' slots (zdec_chunk_append).
+    qkv [T, (n_q + 2 n_kv) * 128] fp32, fp16 or bf16 (rows may be strided),
+    positions [axes, T] or [T] int32, slots [T] int64 (negative: no K/V),
+    q_out [T, n_q, 128] fp16 or bf16 (or None: qkv holds no queries); sections:
+    rotary pairs per position axis (sum 64); rope_theta 0: no rotation;
+    status: optional int32 [1].  Asynchronous."""
+    lib, dev, nkv = load_library(), cache.device, cache.n_kv_heads
+    _tensor(qkv, "qkv", ("float32", "float16", "bfloat16"), (None, None), dev, strided=True)
+    T, width = qkv.shape
+    nq = 0 if q_out is None else q_out.shape[1] if q_out.dim() == 3 else -1
+    if width != (nq + 2 * nkv) * 128:
+        raise ZdecError(-1, f"qkv rows of {width} elements do not hold {nq} query and 2 * {nkv} K/V heads of 128")
+    if q_out is not None:
+        _tensor(q_out, "q_out", ("float16", "bfloat16"), (T, nq, 128), dev, strided=True)
+    axes = len(sections)
+    if not 1 <= axes <= 4:
+        raise ZdecError(-1, "sections must have 1 to 4 entries")
+    _tensor(positions, "positions", ("int32",), (T,) if positions.dim() == 1 and axes == 1 else (axes, T), dev)
+    _tensor(slots, "slots", ("int64",), (T,), dev)
+    rope = _Rope(rope_theta, axes, (ctypes.c_int * 4)(*sections))
+    _call(dev, stream, lib.zdec_chunk_append, cache._ref, layer, ctypes.byref(rope), T, nq, qkv.data_ptr(),
+          _TYPE_ID[str(qkv.dtype)[6:]], _row(qkv), positions.data_ptr(), slots.data_ptr(),
+          None if q_out is None else q_out.data_ptr(), F16 if q_out is None else _TYPE_ID[str(q_out.dtype)[6:]],
+          0 if q_out is None else _row(q_out), _opt(status, "status", ("int32",), (1,), dev))
+
+
+def _row(x) -> int:
+    """Elements from row to row (a single row's own length: its stride says nothing)."""
+    return x.stride(0) if x.shape[0] > 1 else x[:1].numel()
+
+
+def chunk_read(cache: KVPool, layer: int, slots, k, v, status=None, stream=None):
+    """K and V of the given slots [T] int64 as fp16 rows k, v [T, n_kv, 128]
+    (zdec_chunk_read); negative slots read as 0.  Asynchronous."""
+    lib, dev = load_library(), cache.device
+    _tensor(slots, "slots", ("int64",), (None,), dev)
+    T = slots.shape[0]
+    _tensor(k, "k", ("float16",), (T, cache.n_kv_heads, 128), dev)
+    _tensor(v, "v", ("float16",), (T, cache.n_kv_heads, 128), dev)
+    _call(dev, stream, lib.zdec_chunk_read, cache._ref, layer, T, slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _opt(status, "status", ("int32",), (1,), dev))
+
+
+def chunk_attention_workspace_bytes(n_q: int, n_kv_heads: int) -> int:
+    return int(load_library().zdec_chunk_attention_workspace_bytes(n_q, n_kv_heads))
+
+
+def chunk_attention(cache: KVPool, layer: int, q, o, cu, kv_len, tables, workspace, causal: bool = True,
+                    window: int = 0, scale: float | None = None, status=None, stream=None):
+    """Attention of the new tokens of R requests over their pages
+    (zdec_chunk_attention).  q, o [T, n_q, 128] fp16 or bf16 (rows may be
+    strided), int32 cu [R + 1], kv_len [R], tables [R, max_pages]; workspace:
+    uint8 CUDA tensor of chunk_attention_workspace_bytes(n_q, n_kv) bytes, one
+    per stream of calls; scale: 1 / sqrt(128) if None.  Asynchronous."""
+    lib, dev = load_library(), cache.device
+    _tensor(q, "q", ("float16", "bfloat16"), (None, None, 128), dev, strided=True)
+    T, nq = q.shape[0], q.shape[1]
+    _tensor(o, "o", (str(q.dtype)[6:],), (T, nq, 128), dev, strided=True)
+    _tensor(kv_len, "kv_len", ("int32",), (None,), dev)
+    R = kv_len.shape[0]
+    _tensor(cu, "cu", ("int32",), (R + 1,), dev)
+    _tensor(tables, "tables", ("int32",), (R, None), dev)
+    _tensor(workspace, "workspace", ("uint8",), (None,), dev)
+    a = _ChunkAttn(nq, R, T, tables.shape[1], _TYPE_ID[str(q.dtype)[6:]], 1 if causal else 0, window,
+                   128 ** -0.5 if scale is None else scale, _row(q), _row(o))
+    _call(dev, stream, lib.zdec_chunk_attention, cache._ref, layer, ctypes.byref(a), cu.data_ptr(), kv_len.data_ptr(),
+          tables.data_ptr(), q.data_ptr(), o.data_ptr(), workspace.data_ptr(), workspace.numel(),
+          _opt(status, "status", ("int32",), (1,), dev))

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/zdec.h"
+#include "chunk.cuh"
 #include "zdec_kernels.cuh"
 
 using namespace zdec;
@@ -151,6 +152,16 @@ static zdec_status fail(zdec_ctx *c, zdec_status s, const char *fmt, ...) {
     va_end(ap);
     if (c) c->err = buf;
     else g_global_error = buf;
+    return s;
+}
+
+zdec_status zdec::fail_global(zdec_status s, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_global_error = buf;
     return s;
 }
 
@@ -613,6 +624,64 @@ extern "C" zdec_status zdec_seq_len(const zdec_ctx *ctx, int seq, int *len) {
     if (!ctx || !len) return fail(nullptr, ZDEC_ERR_ARG, "null argument");
     if (seq < 0 || seq >= ctx->max_B) return ZDEC_ERR_ARG;
     *len = ctx->len_host[seq];
+    return ZDEC_OK;
+}
+
+// The cache of a context for the chunk operators.
+extern "C" zdec_status zdec_get_cache(const zdec_ctx *ctx, zdec_cache_view *view) {
+    if (!ctx || !view) return fail(nullptr, ZDEC_ERR_ARG, "null argument");
+    view->pool.base = ctx->pool.base;
+    view->pool.n_pages = ctx->pool.n_pages;
+    view->pool.n_layers = ctx->pool.n_layers;
+    view->pool.n_kv_heads = ctx->pool.n_kv;
+    view->pool.k_type = ctx->k_type;
+    view->pool.v_type = ctx->v_type;
+    view->tables = ctx->table_dev;
+    view->lengths = ctx->len_dev;
+    view->max_slots = ctx->max_B;
+    view->max_pages = ctx->max_pages;
+    view->stream = (void *)ctx->stream;
+    return ZDEC_OK;
+}
+
+extern "C" zdec_status zdec_extend(zdec_ctx *ctx, int n, const int32_t *slots, const int32_t *n_new) {
+    if (!ctx) return fail(nullptr, ZDEC_ERR_ARG, "null context");
+    if (n < 0 || n > ctx->max_B || (n > 0 && (!slots || !n_new))) return fail(ctx, ZDEC_ERR_ARG, "bad slot count or null arrays");
+    bool used[MAX_B] = {};
+    for (int i = 0; i < n; i++) {
+        const int s = slots[i];
+        if (s < 0 || s >= ctx->max_B) return fail(ctx, ZDEC_ERR_ARG, "slots[%d] = %d outside [0, %d)", i, s, ctx->max_B);
+        if (used[s]) return fail(ctx, ZDEC_ERR_ARG, "slot %d appears twice", s);
+        used[s] = true;
+        if (n_new[i] < 0) return fail(ctx, ZDEC_ERR_ARG, "n_new[%d] = %d is negative", i, n_new[i]);
+        if ((long)ctx->len_host[s] + n_new[i] > ctx->max_L)
+            return fail(ctx, ZDEC_ERR_CAPACITY, "slot %d: %d + %d tokens exceed max_L %d", s, ctx->len_host[s], n_new[i], ctx->max_L);
+    }
+    try {
+        CK(cudaStreamSynchronize(ctx->stream));   // the lengths below are read by the copies until the second wait
+        std::vector<int> fresh;
+        std::vector<int32_t> len(ctx->len_host.begin(), ctx->len_host.end());
+        for (int i = 0; i < n; i++) {
+            const zdec_status ps = take_pages(ctx, slots[i], len[slots[i]], (long)len[slots[i]] + n_new[i], fresh);
+            if (ps != ZDEC_OK) {   // the pages of the slots before go back
+                give_back_pages(ctx, fresh);
+                return ps;
+            }
+            len[slots[i]] += n_new[i];
+        }
+        cudaError_t e = push_pages(ctx, fresh);
+        for (int i = 0; i < n && e == cudaSuccess; i++)
+            e = cudaMemcpyAsync(ctx->len_dev + slots[i], &len[slots[i]], 4, cudaMemcpyHostToDevice, ctx->stream);
+        const cudaError_t e2 = cudaStreamSynchronize(ctx->stream);
+        if (e == cudaSuccess) e = e2;
+        if (e != cudaSuccess) {
+            give_back_pages(ctx, fresh);
+            return fail(ctx, ZDEC_ERR_CUDA, "extend: %s", cudaGetErrorString(e));
+        }
+        for (int i = 0; i < n; i++) ctx->len_host[slots[i]] = len[slots[i]];
+    } catch (const std::exception &) {
+        return fail(ctx, ZDEC_ERR_OOM, "extend: out of host memory");
+    }
     return ZDEC_OK;
 }
 
