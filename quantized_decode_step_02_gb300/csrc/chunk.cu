@@ -419,6 +419,12 @@ cudaError_t launch_chunk_append(ChunkAppendParams p, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ read ---
+// A stored Q8_0 code times its scale, exact in fp32, at most fp16's largest
+// value (127 x a scale of 516 lies past it).
+__device__ __forceinline__ float q8_value(float scale, uint32_t code) {
+    const float x = scale * (float)((int)code - 128);
+    return x > 65504.0f ? 65504.0f : (x < -65504.0f ? -65504.0f : x);
+}
 // One warp per (token, kv head), lane l: dims 4l .. 4l + 3 of K and V.
 __global__ void chunk_read_kernel(const KvPool a, int layer, int T, const int64_t *__restrict__ slots,
                                   uint16_t *__restrict__ k, uint16_t *__restrict__ v, uint32_t *status) {
@@ -441,7 +447,7 @@ __global__ void chunk_read_kernel(const KvPool a, int layer, int T, const int64_
             } else {
                 const float s = __half2float(*reinterpret_cast<const __half *>(kr + ks_off(tl, lane >> 3)));
                 float f[4];
-                for (int e = 0; e < 4; e++) f[e] = s * (float)((int)((c >> (8 * e)) & 255u) - 128);
+                for (int e = 0; e < 4; e++) f[e] = q8_value(s, (c >> (8 * e)) & 255u);
                 ko = make_uint2(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]));
             }
         }
@@ -453,7 +459,7 @@ __global__ void chunk_read_kernel(const KvPool a, int layer, int T, const int64_
             else {
                 const uint8_t c = vr[v8_off(tl, d + e)];
                 e4[e] = a.v_type == KV_T_FP8 ? (uint16_t)(e4m3x2_to_h2(c) & 0xFFFFu)
-                                             : __half_as_ushort(__float2half_rn(s * (float)((int)c - 128)));
+                                             : __half_as_ushort(__float2half_rn(q8_value(s, c)));
             }
         }
         vo = make_uint2((uint32_t)e4[0] | ((uint32_t)e4[1] << 16), (uint32_t)e4[2] | ((uint32_t)e4[3] << 16));

@@ -442,7 +442,10 @@ def test_attention_non_finite_keys_and_values_stay_with_the_queries_that_see_the
         a, b = clean.run(True, w), dirty.run(True, w)
         i = torch.arange(n, device=DEV) + kv - n
         sees = ((i >= at) & (i < at + w) if w else i >= at) | (i == kv - 1)
-        assert torch.equal(a[~sees], b[~sees])
+        # the same products in fp32, perhaps summed in another order (2^-16 of sum |p v|, at most max |v| < 5), each
+        # then rounded to fp16 by half a step
+        x, y = a[~sees].double(), b[~sees].double()
+        assert y.isfinite().all() and ((x - y).abs() <= 2 * U[torch.float16] * x.abs() + 5 * 2.0 ** -15).all()
         k_bad = types[0] == 0 or bad != bad
         if k_bad:
             assert b[sees & (i < kv - 1)].isnan().any()
