@@ -37,6 +37,7 @@ cudaError_t launch_chunk_read(const KvPool &kv, int layer, int T, const int64_t 
 struct ChunkAttnParams {
     KvPool kv;                     // table: [R][max_pages]
     int layer, nq, G, R, T, io_type, causal, window;
+    int rows;                      // rows of an item: 128 or 256 (set by the launcher)
     float scale_log2;              // scale * log2(e)
     long long q_ld, o_ld;
     const int32_t *cu, *kv_len;

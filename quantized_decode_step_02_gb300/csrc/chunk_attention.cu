@@ -8,12 +8,14 @@
 //   P = exp2(c S - m)  in registers, one row per thread; m lags the maximum by
 //                      at most 2^8 so that O is rarely rescaled
 //   O += P V           tcgen05, P (fp16) in TMEM over S, V in shared memory
-// A CTA (one per SM, persistent) holds two tiles of 128 rows, so that one
-// tile's softmax runs while the tensor core works on the other.  TMEM: S/P of
-// both tiles 2 x 128 columns, O of both 2 x 128: all 512.
+// A CTA (one per SM, persistent) works on two buffers (S/P and O of 128 rows
+// each, all 512 columns of TMEM): the two tiles of 128 rows of an item, or, for
+// an item of at most 128 rows, its even and its odd chunks, joined at the end.
+// So a softmax runs while the tensor core works on the other buffer.
 //
-// Warps: 0 copies (TMA), 1 issues the MMAs, 2 walks the line, 4-7 and 8-11 are the softmax of
-// tile 0 and 1, 12-15 prepare K and V.
+// Warps: 0 copies (TMA), 1 issues the MMAs (one thread), 2 walks the line, 4-7
+// and 8-11 are the softmax of buffer 0 and 1 (a row per thread), 12-15 prepare
+// K and V.
 //
 // The page layout is what the MMA reads: V^T rows of 32 tokens, 64 bytes,
 // swizzled as the 64-byte K-major operand; K rows of 256 bytes, whose two
@@ -29,6 +31,8 @@
 // joins them in key order, so the result does not depend on timing.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "chunk.cuh"
 #include "chunk_sched.cuh"
 #include "tcgen05.cuh"
@@ -38,10 +42,17 @@ namespace zdec {
 constexpr uint32_t CAF = 0xFFFFFFFFu;
 constexpr int CA_THREADS = 512, CA_MAX_CTAS = 160;
 constexpr int CA_SLOT = 32768;                     // bytes of a K or V operand chunk
-constexpr int CA_RAW = 2 * 8704;                   // bytes of two raw one-byte regions
-constexpr int CA_MAX_SLOTS = 5, CA_MAX_RAW = 3;    // fp16 cache: 5 operand slots; else 3 and 3 raw ones
-constexpr int CA_Q_BYTES = 2 * 32768;
-constexpr int CA_SMEM = 1024 + CA_Q_BYTES + CA_MAX_SLOTS * CA_SLOT;
+constexpr int CA_RAW = 8704;                       // bytes of a raw one-byte region (one page's K or V)
+constexpr int CA_MAX_SLOTS = 6, CA_MAX_RAW = 7;
+// Shared memory: Q (rows x 256 bytes), operand slots, raw slots.  An fp16 cache
+// needs no raw slots; a one-byte chunk in flight is half an operand.
+template <int ROWS, bool ALL_F16>
+struct CaLayout {
+    static constexpr int Q_BYTES = ROWS * 256;
+    static constexpr int SLOTS = ALL_F16 ? (ROWS > 128 ? 5 : 6) : (ROWS > 128 ? 3 : 4);
+    static constexpr int RAWS = ALL_F16 ? 0 : (ROWS > 128 ? 6 : 7);
+    static constexpr int BYTES = Q_BYTES + SLOTS * CA_SLOT + RAWS * CA_RAW;
+};
 constexpr long long CA_WAIT_LIMIT = 1LL << 32;     // clock cycles (~2 s)
 constexpr float CA_LAG = 8.0f;                     // log2 units that m may lag behind the maximum
 constexpr int PART_LD = HD + 4;                    // floats of a partial row: m, l, -, -, o[128]
@@ -89,7 +100,7 @@ __device__ __forceinline__ ChunkReq load_req(const ChunkAttnParams &p, int r) {
     q.neff = a >= 0 ? max(0, min(b, p.T) - a) : 0;
     q.causal = p.causal;
     q.window = p.window;
-    q.TP = CA_ROWS / p.G;
+    q.TP = p.rows / p.G;
     q.a = (long long)q.kv - ((long long)b - a);
     return q;
 }
@@ -150,18 +161,38 @@ __device__ __forceinline__ bool partly_seen(const Seen &k, long long key0) {
 
 // ---------------------------------------------------------------- shared ---
 struct CaShared {
+    float2 odd[128];               // (m, l) of each row over the odd chunks of an item with one tile
     uint64_t full[CA_MAX_SLOTS], ready[CA_MAX_SLOTS], empty[CA_MAX_SLOTS];
     uint64_t raw_full[CA_MAX_RAW], raw_empty[CA_MAX_RAW];
-    uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], drain;
+    uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;   // p_ready: keys 0-63, 64-127
+    uint64_t odd_full[4], odd_read[4];   // per softmax warp: `odd` written, and O of the odd chunks read
     uint64_t seg_full[CA_SEGS], seg_empty[CA_SEGS];
     Segment seg[CA_SEGS];
+    Walk walk;
+    long long scan[CA_THREADS / 32];
     uint32_t tmem;
     int abort;
     int pages_ok[8];          // chunk i (mod 8): bit k, page k of it is in the pool
     uint32_t bad[8];          // one byte per preparing warp: a value that only some rows see is not finite
-    int w_r, w_h, w_j, w_off;
-    long long scan[CA_THREADS / 32], total;
 };
+constexpr int CA_SHARED_BYTES = (int)((sizeof(CaShared) + 15) / 16 * 16);
+
+// K and V of an item's chunks in the order they are used: with two tiles
+// K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 ... (its scores run a chunk ahead).
+__device__ __forceinline__ int k_item(int c, bool two) { return two ? 2 * c : (c == 0 ? 0 : 2 * c - 1); }
+__device__ __forceinline__ int v_item(int c, int n_c, bool two) { return two ? 2 * c + 1 : min(2 * c + 2, 2 * n_c - 1); }
+__device__ __forceinline__ void item_at(int i, int n_c, bool two, int &kv, int &c) {
+    if (two) {
+        kv = i & 1;
+        c = i >> 1;
+    } else if (i == 0 || i == 2 * n_c - 1) {
+        kv = i != 0;
+        c = kv ? n_c - 1 : 0;
+    } else {
+        kv = !(i & 1);
+        c = kv ? i / 2 - 1 : (i + 1) / 2;
+    }
+}
 
 struct Waiter {
     volatile int *abort;
@@ -224,10 +255,11 @@ __device__ __forceinline__ void codes16(uint4 c, uint4 &lo, uint4 &hi) {
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
-// code * scale, at most fp16's largest value (127 x a scale of 516 rounds past it); a NaN stays one
-__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
-    const __half2 top = __float2half2_rn(65504.0f);
-    return h2_as_u32(__hmin2_nan(__hmax2_nan(__hmul2(u32_as_h2(a), u32_as_h2(b)), __hneg2(top)), top));
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) { return h2_as_u32(__hmul2(u32_as_h2(a), u32_as_h2(b))); }
+// Two Q8_0 scales, at most 515.5: 127 x 516, which only a block that reaches
+// 65,488 has, is past fp16.  A NaN stays one.
+__device__ __forceinline__ uint32_t q8_scales(uint32_t s) {
+    return h2_as_u32(__hmin2_nan(u32_as_h2(s), __float2half2_rn(515.5f)));
 }
 __device__ __forceinline__ uint4 hmul8(uint4 a, uint4 b) {
     return make_uint4(hmul2_u(a.x, b.x), hmul2_u(a.y, b.y), hmul2_u(a.z, b.z), hmul2_u(a.w, b.w));
@@ -244,55 +276,53 @@ __device__ __forceinline__ uint4 keep8(uint4 v, int lo, int hi) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// K: thread = key of the chunk (0..127); both raw pages -> [half][128 keys][128 bytes], SW128.
+// K of one page: thread = (key, half of the dims) -> [half][keys][128 bytes], SW128; `page`: the chunk's page.
 template <bool Q8>
-__device__ __forceinline__ void prepare_k(const uint8_t *raw, uint8_t *slot, int key) {
-    const int t = key & 63;
-    const uint8_t *reg = raw + (key >> 6) * kv_region_bytes(Q8 ? KV_T_Q8 : KV_T_FP8);
-    uint2 sc = make_uint2(0u, 0u);
-    if (Q8) sc = *reinterpret_cast<const uint2 *>(reg + ks_off(t, 0));
+__device__ __forceinline__ void prepare_k(const uint8_t *reg, uint8_t *slot, int th, int page) {
+    const int t = th & 63, half = th >> 6;
+    uint32_t sc = 0;
+    if (Q8) sc = q8_scales(*reinterpret_cast<const uint32_t *>(reg + ks_off(t, 2 * half)));
+    uint8_t *row = slot + half * 16384 + (page * 64 + t) * 128;
+    uint4 c[4];
 #pragma unroll
-    for (int s = 0; s < 8; s++) {   // 16 dims
+    for (int s = 0; s < 4; s++) c[s] = *reinterpret_cast<const uint4 *>(reg + k8_off(t, 64 * half + 16 * s));
+#pragma unroll
+    for (int s = 0; s < 4; s++) {   // 16 dims
         uint4 lo, hi;
-        codes16<Q8>(*reinterpret_cast<const uint4 *>(reg + k8_off(t, 16 * s)), lo, hi);
+        codes16<Q8>(c[s], lo, hi);
         if (Q8) {
-            const uint32_t two = s < 4 ? sc.x : sc.y, d = (s >> 1) & 1 ? (two >> 16) : (two & 0xFFFFu), dd = d | (d << 16);
-            const uint4 d4 = make_uint4(dd, dd, dd, dd);
+            const uint32_t d = s < 2 ? __byte_perm(sc, sc, 0x1010) : __byte_perm(sc, sc, 0x3232);
+            const uint4 d4 = make_uint4(d, d, d, d);
             lo = hmul8(lo, d4);
             hi = hmul8(hi, d4);
         }
-        uint8_t *row = slot + (s >> 2) * 16384 + key * 128;
-        const int g = 2 * (s & 3);
-        *reinterpret_cast<uint4 *>(row + ((g ^ (t & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4 *>(row + (((g + 1) ^ (t & 7)) << 4)) = hi;
+        *reinterpret_cast<uint4 *>(row + (((2 * s) ^ (t & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4 *>(row + (((2 * s + 1) ^ (t & 7)) << 4)) = hi;
     }
 }
-// V: thread = dim; both raw pages -> [unit of 32 tokens][128 dims][64 bytes],
-// SW64, tokens outside [lo, hi) of the chunk or of a missing page zero.
+// V of one page: thread = dim -> [unit of 32 tokens][128 dims][64 bytes], SW64.
 template <bool Q8>
-__device__ __forceinline__ void prepare_v(const uint8_t *raw, uint8_t *slot, int d, int lo, int hi, int pages_ok) {
+__device__ __forceinline__ void prepare_v(const uint8_t *reg, uint8_t *slot, int d, int page) {
+    uint4 c[4];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-        const uint8_t *reg = raw + (u >> 1) * kv_region_bytes(Q8 ? KV_T_Q8 : KV_T_FP8);
-        const bool there = (pages_ok >> (u >> 1)) & 1;
+    for (int i = 0; i < 4; i++) c[i] = *reinterpret_cast<const uint4 *>(reg + v8_off(16 * i, d));
 #pragma unroll
-        for (int s = 0; s < 2; s++) {   // 16 tokens
-            const int t = 32 * (u & 1) + 16 * s, c0 = 32 * u + 16 * s;   // within the page, within the chunk
-            uint4 a, b;
-            codes16<Q8>(*reinterpret_cast<const uint4 *>(reg + v8_off(t, d)), a, b);
-            if (Q8) {
-                a = hmul8(a, *reinterpret_cast<const uint4 *>(reg + vs_off(t, d >> 5)));
-                b = hmul8(b, *reinterpret_cast<const uint4 *>(reg + vs_off(t + 8, d >> 5)));
-            }
-            a = there ? keep8(a, lo - c0, hi - c0) : make_uint4(0u, 0u, 0u, 0u);
-            b = there ? keep8(b, lo - c0 - 8, hi - c0 - 8) : make_uint4(0u, 0u, 0u, 0u);
-            uint8_t *row = slot + u * 8192 + d * 64;
-            *reinterpret_cast<uint4 *>(row + (((2 * s) ^ ((d >> 1) & 3)) << 4)) = a;
-            *reinterpret_cast<uint4 *>(row + (((2 * s + 1) ^ ((d >> 1) & 3)) << 4)) = b;
+    for (int i = 0; i < 4; i++) {   // 16 tokens
+        uint4 a, b;
+        codes16<Q8>(c[i], a, b);
+        if (Q8) {
+            const uint4 s0 = *reinterpret_cast<const uint4 *>(reg + vs_off(16 * i, d >> 5));
+            const uint4 s1 = *reinterpret_cast<const uint4 *>(reg + vs_off(16 * i + 8, d >> 5));
+            a = hmul8(a, make_uint4(q8_scales(s0.x), q8_scales(s0.y), q8_scales(s0.z), q8_scales(s0.w)));
+            b = hmul8(b, make_uint4(q8_scales(s1.x), q8_scales(s1.y), q8_scales(s1.z), q8_scales(s1.w)));
         }
+        uint8_t *row = slot + (2 * page + (i >> 1)) * 8192 + d * 64;
+        const int g = 2 * (i & 1);
+        *reinterpret_cast<uint4 *>(row + ((g ^ ((d >> 1) & 3)) << 4)) = a;
+        *reinterpret_cast<uint4 *>(row + (((g + 1) ^ ((d >> 1) & 3)) << 4)) = b;
     }
 }
-// fp16 V that landed as an operand: the same zeroing in place.
+// V values outside tokens [lo, hi) of the chunk, or of a missing page, to 0.
 __device__ __forceinline__ void clean_v(uint8_t *slot, int d, int lo, int hi, int pages_ok) {
     for (int u = 0; u < 4; u++) {
         const bool there = (pages_ok >> (u >> 1)) & 1;
@@ -321,50 +351,46 @@ __device__ __forceinline__ float v_at(const uint8_t *slot, int j, int d) {
                                                           ((((j & 31) >> 3) ^ ((d >> 1) & 3)) << 4) + (j & 7) * 2));
 }
 
-// One row of Q: fp16 as it is, bf16 scaled by a power of two into fp16's range
-// (exact but for elements below 2^-28 of the row's largest).  Returns the
-// exponent taken out.
-__device__ __forceinline__ int load_q_row(const ChunkAttnParams &p, const uint16_t *src, bool valid, uint8_t *tile, int row) {
-    uint8_t *dst = tile + row * 128;
-    auto put = [&](int c, uint4 v) {
-        *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = v;
-    };
-    if (!valid) {
-#pragma unroll
-        for (int c = 0; c < 16; c++) put(c, make_uint4(0u, 0u, 0u, 0u));
-        return 0;
-    }
-    const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
-    if (p.io_type == ZDEC_F16) {
-#pragma unroll
-        for (int c = 0; c < 16; c++) put(c, __ldg(s4 + c));
-        return 0;
-    }
-    uint32_t top = 0;   // largest magnitude bits of the row
+// The exponent taken out of a row of Q: 0 for fp16; bf16 goes into the operand
+// times 2^-e, which brings the row's largest element below fp16's top (exact
+// but for elements below 2^-28 of it).
+__device__ __forceinline__ int q_exponent(const uint4 *src, int io_type) {
+    if (io_type == ZDEC_F16) return 0;
+    uint32_t top = 0;   // largest magnitude bits
 #pragma unroll
     for (int c = 0; c < 16; c++) {
-        const uint4 v = __ldg(s4 + c);
+        const uint4 v = __ldg(src + c);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; i++) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
     }
     const int ex = (int)(top >> 7);   // biased exponent
-    const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
-    const float f = exp2f((float)-e);   // e in [-140, 113]; 2^140 is past fp32: two steps below
-    const float f1 = e < -100 ? exp2f(100.0f) : f, f2 = e < -100 ? exp2f((float)(-e - 100)) : 1.0f;
+    return ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
+}
+__device__ __forceinline__ void store_q(const uint4 *src, int io_type, int e, uint8_t *tile, int row) {
+    const float f1 = exp2f((float)min(-e, 100)), f2 = exp2f((float)max(-e - 100, 0));   // e in [-140, 113]: 2^140 in two steps
 #pragma unroll
     for (int c = 0; c < 16; c++) {
-        const uint4 v = __ldg(s4 + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
+        uint4 x = __ldg(src + c);
+        if (io_type != ZDEC_F16) {
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            o[i] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2));
-        put(c, make_uint4(o[0], o[1], o[2], o[3]));
+            for (int i = 0; i < 4; i++)
+                w[i] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2));
+            x = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
     }
-    return e;
 }
-
+// Two fp32 at a time.
+__device__ __forceinline__ void fma_pair(float &x, float &y, float a, float b) {   // x, y = x a + b, y a + b
+    asm("{\n .reg .b64 v, m, c;\n mov.b64 v, {%0, %1};\n mov.b64 m, {%2, %2};\n mov.b64 c, {%3, %3};\n"
+        " fma.rn.f32x2 v, v, m, c;\n mov.b64 {%0, %1}, v;\n}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_pair(float &x, float &y, float a, float b) {
+    asm("{\n .reg .b64 v, c;\n mov.b64 v, {%0, %1};\n mov.b64 c, {%2, %3};\n add.rn.f32x2 v, v, c;\n mov.b64 {%0, %1}, v;\n}"
+        : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
 // 32 fp32 values of a row, times inv, as fp16 or bf16.
 __device__ __forceinline__ void store_o32(uint16_t *dst, const float *v, float inv, int io_type) {
 #pragma unroll
@@ -381,85 +407,67 @@ __device__ __forceinline__ void store_o32(uint16_t *dst, const float *v, float i
 }
 
 // ------------------------------------------------------------------ kernel ---
+__device__ __forceinline__ long long div_small(long long a, int b) {   // a >= 0, b > 0
+    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+template <int ROWS, bool ALL_F16>
 __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __grid_constant__ ChunkAttnParams p,
                                                                         const __grid_constant__ CUtensorMap k_map) {
-    extern __shared__ uint8_t dyn[];
-    __shared__ CaShared sh;
+    extern __shared__ __align__(1024) uint8_t dyn[];   // no static shared memory: starts on a 1024-byte boundary
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
-    const bool k16 = p.kv.k_type == KV_T_F16, v16 = p.kv.v_type == KV_T_F16;
-    const int NS = k16 && v16 ? CA_MAX_SLOTS : 3;
-    uint8_t *q_smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-    uint8_t *slots = q_smem + CA_Q_BYTES, *raws = slots + 3 * CA_SLOT;
+    const bool k16 = ALL_F16 || p.kv.k_type == KV_T_F16, v16 = ALL_F16 || p.kv.v_type == KV_T_F16;
+    using Lay = CaLayout<ROWS, ALL_F16>;
+    constexpr uint32_t NS = Lay::SLOTS, NR = Lay::RAWS > 0 ? Lay::RAWS : 1;
+    uint8_t *q_smem = dyn, *slots = dyn + Lay::Q_BYTES, *raws = slots + NS * CA_SLOT;
+    CaShared &sh = *reinterpret_cast<CaShared *>(dyn + Lay::BYTES);
     CaDesc *desc = reinterpret_cast<CaDesc *>(p.ws) + cta;
 
     // ---- this CTA's piece of the line
-    long long W = 0;
-    for (int r0 = 0; r0 < p.R; r0 += CA_THREADS) {
-        long long w = 0;
-        if (r0 + tid < p.R) {
-            const ChunkReq q = load_req(p, r0 + tid);
-            w = q.before(q.blocks());
-        }
-        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(CAF, w, o);
-        if (lane == 0) sh.scan[warp] = w;
-        __syncthreads();
-        for (int i = 0; i < CA_THREADS / 32; i++) W += sh.scan[i];
-        __syncthreads();
+    const int n_kv = p.kv.n_kv;
+    ChunkReq mine;
+    long long my_w = 0, W = 0;   // the weight of this thread's request of the last strip; all requests' together
+    for (int r = tid; r < p.R; r += CA_THREADS) {
+        mine = load_req(p, r);
+        my_w = mine.before(mine.blocks()) * n_kv;
+        W += my_w;
     }
-    W *= p.kv.n_kv;
-    const int P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has work: pieces follow each other
-    const long long u0 = cta < P ? W * cta / P : 0, u1 = cta < P ? W * (cta + 1) / P : 0;
+    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(CAF, W, o);
+    if (lane == 0) sh.scan[warp] = W;
     if (tid == 0) {
         desc->valid = 0;
         sh.abort = 0;
     }
-    if (u0 >= u1) {
+    __syncthreads();
+    W = 0;
+    for (int i = 0; i < CA_THREADS / 32; i++) W += sh.scan[i];
+    const int P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has work: pieces follow each other
+    if (cta >= P) {
         pdl_launch_dependents();
         return;
     }
-    long long base = 0;
-    for (int r0 = 0; r0 < p.R; r0 += CA_THREADS) {
-        ChunkReq q;
-        long long w = 0;
-        if (r0 + tid < p.R) {
-            q = load_req(p, r0 + tid);
-            w = q.before(q.blocks()) * p.kv.n_kv;
-        }
-        long long incl = w;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(CAF, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) sh.scan[warp] = incl;
-        __syncthreads();
-        long long excl = base + incl - w;
-        for (int i = 0; i < warp; i++) excl += sh.scan[i];
-        if (w > 0 && excl <= u0 && u0 < excl + w) {
-            const long long per = w / p.kv.n_kv, x = u0 - excl;
-            sh.w_r = r0 + tid;
-            sh.w_h = (int)(x / per);
-            sh.w_j = q.block_at(x % per);
-            sh.w_off = (int)(x % per - q.before(sh.w_j));
-        }
-        for (int i = 0; i < CA_THREADS / 32; i++) base += sh.scan[i];
-        __syncthreads();
-        if (base > u0) break;
-    }
+    const long long u0 = div_small(W * cta, P), u1 = div_small(W * (cta + 1), P);
+    if (warp == 1) tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&sh.odd_full[i], 1);
+            mbar_init(&sh.odd_read[i], 1);
+        }
         for (int i = 0; i < CA_MAX_SLOTS; i++) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.ready[i], 4);
             mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < CA_MAX_RAW; i++) {
+        for (uint32_t i = 0; i < NR; i++) {
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 4);
         }
         for (int t = 0; t < 2; t++) {
             mbar_init(&sh.q_ready[t], 4);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_ready[t], 4);
+            mbar_init(&sh.p_ready[t][0], 4);
+            mbar_init(&sh.p_ready[t][1], 4);
             mbar_init(&sh.o_done[t], 1);
         }
         mbar_init(&sh.drain, 1);
@@ -469,11 +477,48 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
         }
         mbar_fence_init();
     }
-    if (warp == 1) tmem_alloc(&sh.tmem, 512);
+    __syncthreads();   // the sums above have been read
+    long long base = 0;
+    for (int r0 = 0; r0 < p.R; r0 += CA_THREADS) {
+        if (p.R > CA_THREADS) {
+            my_w = 0;
+            if (r0 + tid < p.R) {
+                mine = load_req(p, r0 + tid);
+                my_w = mine.before(mine.blocks()) * n_kv;
+            }
+        }
+        long long incl = my_w;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(CAF, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh.scan[warp] = incl;
+        __syncthreads();
+        long long excl = base + incl - my_w;
+        for (int i = 0; i < CA_THREADS / 32; i++) {
+            const long long v = sh.scan[i];
+            if (i < warp) excl += v;
+            base += v;
+        }
+        if (my_w > 0 && excl <= u0 && u0 < excl + my_w) {
+            const long long per = div_small(my_w, n_kv), x = u0 - excl;
+            Walk w;
+            w.q = mine;
+            w.r = r0 + tid;
+            w.J = mine.blocks();
+            w.h = (int)((x >> 32) == 0 && (per >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)per) : x / per);
+            w.j = mine.block_at(x - w.h * per);
+            w.off = (int)(x - w.h * per - mine.before(w.j));
+            w.left = u1 - u0;
+            sh.walk = w;
+        }
+        __syncthreads();
+        if (base > u0) break;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = __shfl_sync(CAF, sh.tmem, 0);
     pdl_launch_dependents();
 
     const Waiter wait{&sh.abort, p.status};
@@ -489,398 +534,466 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
         si++;
     };
 
+    // registers: 4 warpgroups x 128 at launch = 64 + 80 + 2 x 184
     if (group == 0) {
-        reg_dec<64>();
-        if (warp == 0) {
-            // ------------------------------------------------------ copies ---
-            const uint32_t kb = kv_region_bytes(p.kv.k_type), vb = kv_region_bytes(p.kv.v_type);
-            const size_t coff = kv_chunk_off(p.kv, p.layer, 0);
-            uint32_t it = 0, dir = 0, raw = 0, ci = 0;   // operands, those landing as such, raw ones; chunks
-            bool ok = true;
-            for (; ok && next(); done()) {
-                const Segment s = sh.seg[si % CA_SEGS];
-                const int32_t *row = p.kv.table + (size_t)s.r * p.kv.max_pages;
-                const size_t off = coff + (size_t)s.h * (kb + vb);
-                int mine = -1;
-                for (int c = 0; ok && c < s.n_c; c++, ci++) {
-                    if ((c & 15) == 0) {   // the pages of the next 16 chunks, one per lane
-                        const long long pg = (long long)(s.c0 + c) * 2 + lane;
-                        mine = pg < p.kv.max_pages && pg * 64 < s.kv ? __ldg(row + pg) : -2;   // -2: no key there
-                    }
-                    const int pa = __shfl_sync(CAF, mine, 2 * (c & 15)), pb = __shfl_sync(CAF, mine, 2 * (c & 15) + 1);
-                    const int okm = (kv_page_ok(p.kv, pa) ? 1 : 0) | (kv_page_ok(p.kv, pb) ? 2 : 0);
-                    if (lane == 0) {
-                        if (p.status && ((!(okm & 1) && pa != -2) || (!(okm & 2) && pb != -2)))
-                            atomicOr(p.status, (uint32_t)ZDEC_CHUNK_NO_PAGE);
-                        for (int kv = 0; ok && kv < 2; kv++, it++) {   // K, then V
-                            const bool direct = kv ? v16 : k16;
-                            const uint32_t bytes = kv ? vb : kb;
-                            uint8_t *dst;
-                            uint64_t *bar;
-                            if (direct) {
-                                const uint32_t sl = it % NS;
-                                ok = it < (uint32_t)NS || wait(&sh.empty[sl], (it / NS - 1) & 1);
-                                dst = slots + sl * CA_SLOT;
-                                bar = &sh.full[dir % CA_MAX_SLOTS];
-                                dir++;
-                            } else {
-                                const uint32_t sl = raw % CA_MAX_RAW;
-                                ok = raw < (uint32_t)CA_MAX_RAW || wait(&sh.raw_empty[sl], (raw / CA_MAX_RAW - 1) & 1);
-                                dst = raws + sl * CA_RAW;
-                                bar = &sh.raw_full[sl];
-                                raw++;
-                            }
-                            if (!ok) break;
-                            // chunk ci's entry was last read for chunk ci - 8, whose operands have left their slots
-                            if (kv == 0) sh.pages_ok[ci & 7] = okm;
-                            const int n = __popc(okm);
-                            if (n) mbar_expect_tx(bar, n * bytes);
+    reg_dec<64>();
+    if (warp == 0) {
+        // ---------------------------------------------------------- copies ---
+        const uint32_t kb = kv_region_bytes(p.kv.k_type), vb = kv_region_bytes(p.kv.v_type);
+        const size_t coff = kv_chunk_off(p.kv, p.layer, 0);
+        uint32_t it = 0, dir = 0, raw = 0, ci = 0;   // operands, those landing as such, raw pages; chunks
+        bool ok = true;
+        for (; ok && next(); done()) {
+            const Segment s = sh.seg[si % CA_SEGS];
+            const bool two = ROWS > 128 && s.rows > 128;
+            const int32_t *row = p.kv.table + (size_t)s.r * p.kv.max_pages;
+            const size_t off = coff + (size_t)s.h * (kb + vb);
+            // pages of 16 chunks, one per lane; V lags K by up to two chunks, so the 16 before are kept
+            auto pages_of = [&](int c16) {
+                const long long pg = ((long long)s.c0 + 16 * c16) * 2 + lane;
+                return pg < p.kv.max_pages && pg * 64 < s.kv ? __ldg(row + pg) : -2;   // -2: no key there
+            };
+            int now = pages_of(0), before = -2, now_i = 0;
+            for (int i = 0; ok && i < 2 * s.n_c; i++, it++) {
+                int kv, c;
+                item_at(i, s.n_c, two, kv, c);
+                if (kv == 0 && (c >> 4) != now_i) {
+                    before = now;
+                    now_i = c >> 4;
+                    now = pages_of(now_i);
+                }
+                const int from = (c >> 4) == now_i ? now : before;
+                const int pa = __shfl_sync(CAF, from, 2 * (c & 15)), pb = __shfl_sync(CAF, from, 2 * (c & 15) + 1);
+                const int okm = (kv_page_ok(p.kv, pa) ? 1 : 0) | (kv_page_ok(p.kv, pb) ? 2 : 0);
+                if (lane == 0) {
+                    const uint32_t bytes = kv ? vb : kb;
+                    const size_t at = off + (kv ? kb : 0);
+                    if (kv ? v16 : k16) {
+                        const uint32_t sl = it % NS;
+                        ok = it < NS || wait(&sh.empty[sl], (it / NS - 1) & 1);
+                        if (ok) {
+                            // chunk ci + c's entry was last read for chunk ci + c - 8, whose operands have left their slots
+                            if (kv == 0) sh.pages_ok[(ci + c) & 7] = okm;
+                            uint8_t *dst = slots + sl * CA_SLOT;
+                            uint64_t *bar = &sh.full[dir % CA_MAX_SLOTS];
+                            dir++;
+                            if (okm) mbar_expect_tx(bar, __popc(okm) * bytes);
                             else mbar_arrive1(bar);
                             for (int k = 0; k < 2; k++) {
                                 if (!((okm >> k) & 1)) continue;
                                 const int page = k ? pb : pa;
-                                const uint8_t *src = p.kv.base + (size_t)page * p.kv.page_bytes + off + (kv ? kb : 0);
-                                if (!direct) bulk_g2s(dst + k * bytes, src, bytes, bar);
-                                else if (kv) bulk_g2s(dst + k * 16384, src, bytes, bar);
+                                if (kv) bulk_g2s(dst + k * 16384, p.kv.base + (size_t)page * p.kv.page_bytes + at, bytes, bar);
                                 else
                                     for (int half = 0; half < 2; half++)
-                                        tma_k_half(dst + half * 16384 + k * 8192, &k_map, half, p.layer * p.kv.n_kv + s.h, page, bar);
+                                        tma_k_half(dst + half * 16384 + k * 8192, &k_map, half, p.layer * n_kv + s.h, page, bar);
                             }
                         }
-                    }
-                    ok = __shfl_sync(CAF, (int)ok, 0);
-                }
-            }
-            // copies in flight land before the CTA leaves, also where a wait gave up
-            if (lane == 0 && sh.abort) {
-                const long long t0 = clock64();
-                for (uint32_t i = dir > (uint32_t)CA_MAX_SLOTS ? dir - CA_MAX_SLOTS : 0; i < dir; i++)
-                    while (!mbar_try_wait(&sh.full[i % CA_MAX_SLOTS], (i / CA_MAX_SLOTS) & 1) && clock64() - t0 < CA_WAIT_LIMIT) {}
-                for (uint32_t i = raw > (uint32_t)CA_MAX_RAW ? raw - CA_MAX_RAW : 0; i < raw; i++)
-                    while (!mbar_try_wait(&sh.raw_full[i % CA_MAX_RAW], (i / CA_MAX_RAW) & 1) && clock64() - t0 < CA_WAIT_LIMIT) {}
-            }
-        } else if (warp == 1) {
-            // ---------------------------------------------------------- MMA ---
-            constexpr uint32_t IDESC = MMA_IDESC_F16<128, 128>;
-            const uint32_t q_addr = smem_u32(q_smem), slot_addr = smem_u32(slots);
-            const bool leader = lane == 0;
-            uint32_t it = 0, ci = 0, segs[2] = {0, 0}, n_p[2] = {0, 0};   // operands, chunks; segments and PVs per tile
-            bool ok = true;
-            auto qk = [&](int t, uint32_t sl) {
-                const uint32_t qa = q_addr + t * 32768, ka = slot_addr + sl * CA_SLOT;
-#pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
-                    mma_ss(tmem + t * 128, mma_desc_sw128(qa + o), mma_desc_sw128(ka + o), IDESC, k > 0);
-                }
-                mma_commit(&sh.s_full[t]);
-            };
-            auto pv = [&](int t, uint32_t sl, bool first, bool bad) {
-                // a chunk whose product the softmax threads make themselves only reports
-                if (bad) { mma_commit(&sh.o_done[t]); return; }
-                const uint32_t va = slot_addr + sl * CA_SLOT;
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, mma_desc_sw64(va + (k >> 1) * 8192 + (k & 1) * 32), IDESC,
-                           !first || k > 0);
-                mma_commit(&sh.o_done[t]);
-            };
-            for (; ok && next(); done()) {
-                const int n_c = sh.seg[si % CA_SEGS].n_c, nt = sh.seg[si % CA_SEGS].rows > 128 ? 2 : 1;
-                if (n_c == 0) continue;
-                for (int t = 0; t < nt; t++) ok = ok && wait.warp(&sh.q_ready[t], segs[t]++ & 1);
-                uint32_t ks = it % NS;
-                ok = ok && wait.warp(&sh.ready[ks], (it / NS) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (leader) {
-                    for (int t = 0; t < nt; t++) qk(t, ks);
-                    mma_commit(&sh.empty[ks]);
-                }
-                it++;
-                for (int c = 0; ok && c < n_c; c++, ci++) {
-                    const uint32_t vi = it, ki = it + 1;   // V of this chunk, K of the next
-                    const bool more = c + 1 < n_c;
-                    ok = wait.warp(&sh.ready[vi % NS], (vi / NS) & 1);
-                    for (int t = 0; ok && t < nt; t++) {
-                        ok = wait.warp(&sh.p_ready[t], n_p[t] & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (leader) {
-                            pv(t, vi % NS, c == 0, sh.bad[ci & 7] != 0);
-                            if (t == nt - 1) mma_commit(&sh.empty[vi % NS]);
-                        }
-                        if (more) {
-                            if (t == 0) ok = wait.warp(&sh.ready[ki % NS], (ki / NS) & 1);
-                            // the next S overwrites the P that this PV reads
-                            ok = ok && wait.warp(&sh.o_done[t], n_p[t] & 1);
+                    } else {
+                        for (int k = 0; ok && k < 2; k++) {
+                            const uint32_t sl = raw % NR;
+                            ok = raw < NR || wait(&sh.raw_empty[sl], (raw / NR - 1) & 1);
                             if (!ok) break;
-                            tc_fence_after();
-                            if (leader) {
-                                qk(t, ki % NS);
-                                if (t == nt - 1) mma_commit(&sh.empty[ki % NS]);
+                            if (kv == 0 && k == 0) sh.pages_ok[(ci + c) & 7] = okm;
+                            uint64_t *bar = &sh.raw_full[sl];
+                            raw++;
+                            if ((okm >> k) & 1) {
+                                mbar_expect_tx(bar, bytes);
+                                bulk_g2s(raws + sl * CA_RAW, p.kv.base + (size_t)(k ? pb : pa) * p.kv.page_bytes + at, bytes, bar);
+                            } else {
+                                mbar_arrive1(bar);
                             }
                         }
-                        n_p[t]++;
                     }
-                    it += more ? 2 : 1;
+                    if (p.status && kv == 0 && ((!(okm & 1) && pa != -2) || (!(okm & 2) && pb != -2)))
+                        atomicOr(p.status, (uint32_t)ZDEC_CHUNK_NO_PAGE);
                 }
+                ok = __shfl_sync(CAF, (int)ok, 0);
+            }
+            ci += s.n_c;
+        }
+        // copies in flight land before the CTA leaves, also where a wait gave up
+        if (lane == 0 && sh.abort) {
+            const long long t0 = clock64();
+            for (uint32_t i = dir > CA_MAX_SLOTS ? dir - CA_MAX_SLOTS : 0; i < dir; i++)
+                while (!mbar_try_wait(&sh.full[i % CA_MAX_SLOTS], (i / CA_MAX_SLOTS) & 1) && clock64() - t0 < CA_WAIT_LIMIT) {}
+            for (uint32_t i = raw > NR ? raw - NR : 0; !ALL_F16 && i < raw; i++)
+                while (!mbar_try_wait(&sh.raw_full[i % NR], (i / NR) & 1) && clock64() - t0 < CA_WAIT_LIMIT) {}
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA ---
+        if (elect_one()) {
+            constexpr uint32_t IDESC = MMA_IDESC_F16<128, 128>;
+            const uint64_t q_desc = mma_desc_sw128(smem_u32(q_smem)), k_desc = mma_desc_sw128(smem_u32(slots)),
+                           v_desc = mma_desc_sw64(smem_u32(slots));
+            uint32_t it0 = 0, ci = 0, segs[2] = {0, 0}, n_p[2] = {0, 0};   // operands, chunks before; segments, steps per buffer
+            bool ok = true;
+            auto ready = [&](uint32_t item) { return wait(&sh.ready[item % NS], (item / NS) & 1); };
+            for (; ok; si++) {
+                ok = wait(&sh.seg_full[si % CA_SEGS], (si / CA_SEGS) & 1);
+                const int n_c = sh.seg[si % CA_SEGS].n_c;
+                const bool two = ROWS > 128 && sh.seg[si % CA_SEGS].rows > 128;
+                if (!ok || n_c < 0) break;
+                mbar_arrive1(&sh.seg_empty[si % CA_SEGS]);
+                if (n_c == 0) continue;
+                const int steps = two ? 2 * n_c : n_c;
+                // S of step i: chunk i / 2 of tile i % 2, or chunk i of the one tile, in buffer i % 2
+                auto qk = [&](int i) {
+                    const int u = i & 1;
+                    const uint32_t item = it0 + k_item(two ? i >> 1 : i, two);
+                    if (!two || u == 0) ok = ok && ready(item);
+                    if (!ok) return;
+                    tc_fence_after();
+                    tc_fence_order();   // S overwrites the P that the PV before reads
+                    const uint64_t qd = q_desc + (two ? u * (32768 >> 4) : 0), kd = k_desc + (item % NS) * (CA_SLOT >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        mma_ss(tmem + u * 128, qd + o, kd + o, IDESC, k > 0);
+                    }
+                    mma_commit(&sh.s_full[u]);
+                    if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                };
+                for (int t = 0; t < (two ? 2 : 1); t++) ok = ok && wait(&sh.q_ready[t], segs[t]++ & 1);
+                if (ok) qk(0);
+                if (ok && steps > 1) qk(1);
+                for (int i = 0; ok && i < steps; i++) {
+                    const int u = i & 1, c = two ? i >> 1 : i;
+                    const uint32_t item = it0 + v_item(c, n_c, two);
+                    if (!two || u == 0) ok = ready(item);
+                    ok = ok && wait(&sh.p_ready[u][0], n_p[u] & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = v_desc + (item % NS) * (CA_SLOT >> 4);
+                    const uint32_t od = tmem + 256 + u * 128;
+                    // a chunk whose product the softmax threads make themselves only reports
+                    const bool bad = sh.bad[(ci + c) & 7] != 0;
+                    if (!bad)
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, i > 1 || k > 0);
+                    ok = wait(&sh.p_ready[u][1], n_p[u] & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (!bad)
+#pragma unroll
+                        for (int k = 4; k < 8; k++)
+                            mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, true);
+                    mma_commit(&sh.o_done[u]);
+                    if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                    n_p[u]++;
+                    if (i + 2 < steps) qk(i + 2);
+                }
+                it0 += 2 * n_c;
+                ci += n_c;
             }
             if (!ok) {   // a wait gave up: MMAs in flight end before the CTA leaves
-                if (leader) mma_commit(&sh.drain);
+                mma_commit(&sh.drain);
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&sh.drain, 0) && clock64() - t0 < CA_WAIT_LIMIT) {}
             }
-        } else if (warp == 2) {
-            // ----------------------------------------------------- the walk ---
-            if (lane == 0) {
-                Walk w;
-                w.r = sh.w_r;
-                w.h = sh.w_h;
-                w.j = sh.w_j;
-                w.off = sh.w_off;
-                w.left = u1 - u0;
-                w.q = load_req(p, w.r);
-                w.J = w.q.blocks();
-                bool more = true;
-                for (uint32_t i = 0; more; i++) {
-                    Segment s;
-                    more = next_segment(p, w, u1, W, P, s);
-                    if (!more) s.n_c = -1;
-                    if (i >= CA_SEGS && !wait(&sh.seg_empty[i % CA_SEGS], (i / CA_SEGS - 1) & 1)) break;
-                    sh.seg[i % CA_SEGS] = s;
-                    mbar_arrive1(&sh.seg_full[i % CA_SEGS]);
-                }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // --------------------------------------------------------- the walk ---
+        if (lane == 0) {
+            Walk w = sh.walk;
+            bool more = true;
+            for (uint32_t i = 0; more; i++) {
+                Segment s;
+                more = next_segment(p, w, u1, W, P, s);
+                if (!more) s.n_c = -1;
+                if (i >= CA_SEGS && !wait(&sh.seg_empty[i % CA_SEGS], (i / CA_SEGS - 1) & 1)) break;
+                sh.seg[i % CA_SEGS] = s;
+                mbar_arrive1(&sh.seg_full[i % CA_SEGS]);
             }
         }
+    }
     } else if (group == 3) {
         // ------------------------------------------------------- preparing ---
-        reg_dec<64>();
+        reg_dec<80>();
         const int th = tid - 384;
         uint32_t it = 0, dir = 0, raw = 0, ci = 0;
         bool ok = true;
         for (; ok && next(); done()) {
             const Segment s = sh.seg[si % CA_SEGS];
+            const bool two = ROWS > 128 && s.rows > 128;
             const Seen seen = seen_by(p, s);
-            for (int c = 0; ok && c < s.n_c; c++, ci++) {
+            for (int i = 0; ok && i < 2 * s.n_c; i++, it++) {
+                int kv, c;
+                item_at(i, s.n_c, two, kv, c);
                 const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
-                const int vlo = (int)max(0LL, seen.lo - key0), vhi = (int)min((long long)CA_KEYS, seen.hi - key0);
-                const bool part = partly_seen(seen, key0);
-                for (int kv = 0; ok && kv < 2; kv++, it++) {
-                    const uint32_t sl = it % NS;
-                    uint8_t *slot = slots + sl * CA_SLOT;
-                    if (kv ? v16 : k16) {
-                        ok = wait.warp(&sh.full[dir % CA_MAX_SLOTS], (dir / CA_MAX_SLOTS) & 1);
-                        if (!ok) break;
-                        dir++;
-                        const int pok = sh.pages_ok[ci & 7];
-                        if (kv && (vlo > 0 || vhi < CA_KEYS || pok != 3)) {
-                            clean_v(slot, th, vlo, vhi, pok);
-                            async_proxy_fence();
-                        }
-                    } else {
-                        const uint32_t rs = raw % CA_MAX_RAW;
-                        ok = wait.warp(&sh.raw_full[rs], (raw / CA_MAX_RAW) & 1) &&
-                             (it < (uint32_t)NS || wait.warp(&sh.empty[sl], (it / NS - 1) & 1));
+                const uint32_t sl = it % NS;
+                uint8_t *slot = slots + sl * CA_SLOT;
+                if (kv ? v16 : k16) {
+                    ok = wait.warp(&sh.full[dir % CA_MAX_SLOTS], (dir / CA_MAX_SLOTS) & 1);
+                    if (!ok) break;
+                    dir++;
+                } else {
+                    ok = it < NS || wait.warp(&sh.empty[sl], (it / NS - 1) & 1);
+                    for (int k = 0; ok && k < 2; k++) {
+                        const uint32_t rs = raw % NR;
+                        ok = wait.warp(&sh.raw_full[rs], (raw / NR) & 1);
                         if (!ok) break;
                         const uint8_t *src = raws + rs * CA_RAW;
                         if (kv) {
-                            const int pok = sh.pages_ok[ci & 7];
-                            if (p.kv.v_type == KV_T_Q8) prepare_v<true>(src, slot, th, vlo, vhi, pok);
-                            else prepare_v<false>(src, slot, th, vlo, vhi, pok);
+                            if (p.kv.v_type == KV_T_Q8) prepare_v<true>(src, slot, th, k);
+                            else prepare_v<false>(src, slot, th, k);
                         } else {
-                            if (p.kv.k_type == KV_T_Q8) prepare_k<true>(src, slot, th);
-                            else prepare_k<false>(src, slot, th);
+                            if (p.kv.k_type == KV_T_Q8) prepare_k<true>(src, slot, th, k);
+                            else prepare_k<false>(src, slot, th, k);
                         }
-                        async_proxy_fence();
                         __syncwarp();
                         if (lane == 0) mbar_arrive1(&sh.raw_empty[rs]);
                         raw++;
                     }
-                    if (kv) {
-                        const bool bad = __any_sync(CAF, part && v_not_finite(slot, th));
-                        if (lane == 0) reinterpret_cast<uint8_t *>(&sh.bad[ci & 7])[warp & 3] = bad;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive1(&sh.ready[sl]);
+                    if (!ok) break;
                 }
+                if (kv) {
+                    const int lo = (int)max(0LL, seen.lo - key0), hi = (int)min((long long)CA_KEYS, seen.hi - key0);
+                    const int pok = sh.pages_ok[(ci + c) & 7];
+                    if (lo > 0 || hi < CA_KEYS || pok != 3) clean_v(slot, th, lo, hi, pok);
+                    const bool bad = __any_sync(CAF, partly_seen(seen, key0) && v_not_finite(slot, th));
+                    if (lane == 0) reinterpret_cast<uint8_t *>(&sh.bad[(ci + c) & 7])[warp & 3] = bad;
+                }
+                async_proxy_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&sh.ready[sl]);
             }
+            ci += s.n_c;
         }
     } else {
         // --------------------------------------------------------- softmax ---
-        reg_inc<192>();
-        const int t = group - 1;                       // tile
-        const int row = tid - 128 - 128 * t;           // row of the tile = TMEM lane
-        const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);   // lanes 32 (warp % 4) ..
-        const uint32_t s_addr = lane_base + t * 128, o_addr = lane_base + 256 + t * 128;
-        uint32_t n_s = 0, ci = 0;                      // chunks of this tile, of the CTA
+        reg_inc<184>();
+        const int u = group - 1, w4 = warp & 3, row = w4 * 32 + lane;     // buffer; TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)w4 << 21);           // lanes 32 (warp % 4) ..
+        const uint32_t s_addr = lane_base + u * 128, o_addr = lane_base + 256 + u * 128;
+        uint32_t n_s = 0, n_odd = 0, it0 = 0, ci = 0;   // steps of this buffer, joins; operands, chunks before
         bool ok = true;
         for (; ok && next(); done()) {
             const Segment &s = sh.seg[si % CA_SEGS];
-            const int n_c = s.n_c;
-            const int first_row = t * 128, my = first_row + row;
-            if (first_row >= s.rows) {                 // no row of this tile in the item
-                ci += n_c;
-                continue;
-            }
-            const bool valid = my < s.rows;
-            const int flat = s.row0 + min(my, s.rows - 1);
-            const int tok = flat / p.G, head = s.h * p.G + flat % p.G;
-            uint16_t *out = p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD;
-            if (n_c == 0) {                            // nothing is seen
-                if (valid) {
+            const int n_c = s.n_c, rows = s.rows;
+            const bool two = ROWS > 128 && rows > 128;
+            const int first = two ? u * 128 : 0;           // this buffer's tile begins at this row of the item
+            if (n_c == 0) {                                // nothing is seen
+                const int my = u * 128 + row;
+                if (my < rows) {
+                    const int flat = s.row0 + my, tok = flat / p.G, head = s.h * p.G + flat - tok * p.G;
+                    uint16_t *out = p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD;
                     const float zero[32] = {};
                     for (int d = 0; d < 4; d++) store_o32(out + 32 * d, zero, 0.0f, p.io_type);
                 }
                 __syncwarp();
                 continue;
             }
-            const int e = load_q_row(p, p.q + (long long)(s.t0 + tok) * p.q_ld + (long long)head * HD, valid,
-                                     q_smem + t * 32768, row);
-            async_proxy_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(&sh.q_ready[t]);
-            const float sc = fmaxf(ldexpf(p.scale_log2, e), 7.9e-31f);   // log2 units per score; never 0 (0 * -inf)
-            const float lag = CA_LAG / sc;
-            const long long pos = s.a + tok;              // keys [klo, khi) of this row
-            const long long khi = p.causal ? min((long long)s.kv, pos + 1) : s.kv;
-            const long long klo = p.window ? pos + 1 - p.window : 0;
+            const bool act = first + w4 * 32 < rows;       // a warp without a row only takes part in the barriers
+            const int flat = s.row0 + min(first + row, rows - 1);   // rows past the last repeat it
+            const int tok = flat / p.G, head = s.h * p.G + flat - tok * p.G;
+            const long long pos = s.a + tok;
+            float scale = 0.0f;                            // log2 units per score
+            if (act) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (long long)(s.t0 + tok) * p.q_ld + (long long)head * HD);
+                const int e = q_exponent(src, p.io_type);
+                if (two || u == 0) store_q(src, p.io_type, e, q_smem + first * 256, row);
+                scale = fmaxf(ldexpf(p.scale_log2, e), 7.9e-31f);   // never 0 (0 * -inf)
+            }
+            if (two || u == 0) {
+                async_proxy_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&sh.q_ready[u]);
+            }
             const Seen seen = seen_by(p, s);
-            float m = -INFINITY, msc = 0.0f, l = 0.0f;   // running maximum (raw), m * sc, sum
-            for (int c = 0; ok && c < n_c; c++, ci++, n_s++) {
-                ok = wait.warp(&sh.s_full[t], n_s & 1);
+            // chunks in [c_a, c_b) are seen whole by every row
+            const int c_a = (int)((seen.all_lo + CA_KEYS - 1) / CA_KEYS) - s.c0, c_b = (int)(seen.all_hi / CA_KEYS) - s.c0;
+            float m = -INFINITY, ms = 0.0f, l = 0.0f;      // running maximum (raw), m * scale, sum
+            const int c_first = two ? 0 : u, c_step = two ? 1 : 2;
+            for (int c = c_first; c < n_c; c += c_step, n_s++) {
+                ok = wait.warp(&sh.s_full[u], n_s & 1);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t v[4][32];
+                if (act) {
+                    uint32_t v[4][32];
 #pragma unroll
-                for (int g = 0; g < 4; g++) tmem_ld32(s_addr + 32 * g, v[g]);
-#pragma unroll
-                for (int g = 0; g < 4; g++) tmem_wait_ld(v[g]);
-                const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
-                const int pok = sh.pages_ok[ci & 7];
-                int lo2 = 0, hi2 = CA_KEYS;
-                uint32_t bad = 0;
-                if (key0 + CA_KEYS > seen.all_hi || key0 < seen.all_lo || pok != 3) {
-                    lo2 = (int)max(0LL, min((long long)CA_KEYS, klo - key0));
-                    hi2 = (int)max(0LL, min((long long)CA_KEYS, khi - key0));
-                    if (!(pok & 1)) lo2 = max(lo2, 64);
-                    if (!(pok & 2)) hi2 = min(hi2, 64);
-                    if (partly_seen(seen, key0)) {       // V has been looked through by now
-                        const uint32_t vi = 2 * ci + 1;
-                        ok = wait.warp(&sh.ready[vi % NS], (vi / NS) & 1);
-                        if (!ok) break;
-                        bad = sh.bad[ci & 7];
-                    }
-#pragma unroll
-                    for (int g = 0; g < 4; g++)
-#pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            if (32 * g + i < lo2 || 32 * g + i >= hi2) v[g][i] = 0xFF800000u;   // -inf
-                }
-                float mx[4];
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    mx[g] = __uint_as_float(v[g][0]);
-#pragma unroll
-                    for (int i = 1; i < 32; i++) mx[g] = fmaxf(mx[g], __uint_as_float(v[g][i]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const bool grow = top > m + lag || (m == -INFINITY && top > m);
-                if (__any_sync(CAF, grow)) {
-                    const float m_new = grow ? top : m, msc_new = grow ? top * sc : msc;
-                    if (c > 0) {
-                        const float f = grow ? (m == -INFINITY ? 0.0f : exp2_approx(msc - msc_new)) : 1.0f;
-                        l *= f;
-                        ok = wait.warp(&sh.o_done[t], (n_s - 1) & 1);   // the PV before has finished
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int g = 0; g < 4; g++) {
-                            uint32_t x[32];
-                            tmem_ld32(o_addr + 32 * g, x);
-                            tmem_wait_ld(x);
-#pragma unroll
-                            for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                            tmem_st32(o_addr + 32 * g, x);
+                    for (int g = 0; g < 4; g++) tmem_ld32(s_addr + 32 * g, v[g]);
+                    const int pok = sh.pages_ok[(ci + c) & 7];
+                    int lo = 0, hi = CA_KEYS;              // keys of the chunk that this row sees
+                    uint32_t bad = 0;
+                    const bool edge = c < c_a || c >= c_b || pok != 3;
+                    if (edge) {
+                        const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
+                        const long long khi = p.causal ? min((long long)s.kv, pos + 1) : s.kv, klo = p.window ? pos + 1 - p.window : 0;
+                        lo = (int)max(0LL, min((long long)CA_KEYS, klo - key0));
+                        hi = (int)max(0LL, min((long long)CA_KEYS, khi - key0));
+                        if (!(pok & 1)) lo = max(lo, 64);
+                        if (!(pok & 2)) hi = min(hi, 64);
+                        if (partly_seen(seen, key0)) {     // V has been looked through by now
+                            const uint32_t vi = it0 + v_item(c, n_c, two);
+                            ok = wait.warp(&sh.ready[vi % NS], (vi / NS) & 1);
+                            bad = sh.bad[(ci + c) & 7];
                         }
                     }
-                    m = m_new;
-                    msc = msc_new;
-                }
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    uint32_t h[16];
+                    for (int g = 0; g < 4; g++) tmem_wait_ld(v[g]);
+                    if (!ok) break;
+                    if (edge) {
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const float a = exp2_approx(fmaf(__uint_as_float(v[g][2 * i]), sc, -msc));
-                        const float b = exp2_approx(fmaf(__uint_as_float(v[g][2 * i + 1]), sc, -msc));
-                        sum[i & 3] += a + b;
-                        h[i] = h2_as_u32(__floats2half2_rn(a, b));
+                        for (int g = 0; g < 4; g++)
+#pragma unroll
+                            for (int k = 0; k < 32; k++)
+                                if (32 * g + k < lo || 32 * g + k >= hi) v[g][k] = 0xFF800000u;   // -inf
                     }
-                    tmem_st16(s_addr + 16 * g, h);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                if (bad) {
-                    // a value that is not finite lies in the chunk and some rows do not see it: 0 times it would be
-                    // NaN, so each row adds up what it sees by itself (rare, and slow)
-                    if (c > 0) {
-                        ok = wait.warp(&sh.o_done[t], (n_s - 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    const uint8_t *vs = slots + ((2 * ci + 1) % NS) * CA_SLOT;
-#pragma unroll 1
+                    float mx[4];
+#pragma unroll
                     for (int g = 0; g < 4; g++) {
-                        uint32_t x[32];
-                        tmem_ld32(o_addr + 32 * g, x);
-                        tmem_wait_ld(x);
-                        if (c == 0)
+                        mx[g] = __uint_as_float(v[g][0]);
 #pragma unroll
-                            for (int i = 0; i < 32; i++) x[i] = 0u;
-#pragma unroll 1
-                        for (int j = 0; j < CA_KEYS; j++) {
-                            const float2 pp = __half22float2(u32_as_h2(tmem_ld1(s_addr + (j >> 1))));
-                            const float pj = j & 1 ? pp.y : pp.x;
-                            const bool mine = j >= lo2 && j < hi2;
-#pragma unroll
-                            for (int i = 0; i < 32; i++)
-                                x[i] = mine ? __float_as_uint(fmaf(pj, v_at(vs, j, 32 * g + i), __uint_as_float(x[i]))) : x[i];
-                        }
-                        tmem_st32(o_addr + 32 * g, x);
+                        for (int k = 1; k < 31; k += 2) mx[g] = fmaxf(fmaxf(mx[g], __uint_as_float(v[g][k])), __uint_as_float(v[g][k + 1]));
+                        mx[g] = fmaxf(mx[g], __uint_as_float(v[g][31]));
                     }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grow = (top - m) * scale > CA_LAG || (m == -INFINITY && top > m);
+                    if (__any_sync(CAF, grow)) {
+                        const float m_new = grow ? top : m, ms_new = grow ? top * scale : ms;
+                        if (c > c_first) {
+                            const float f = grow ? (m == -INFINITY ? 0.0f : exp2_approx(ms - ms_new)) : 1.0f;
+                            l *= f;
+                            ok = wait.warp(&sh.o_done[u], (n_s - 1) & 1);   // the PV before has finished
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int g = 0; g < 8; g++) {
+                                uint32_t x[16];
+                                tmem_ld16(o_addr + 16 * g, x);
+#pragma unroll
+                                for (int k = 0; k < 16; k++) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                                tmem_st16(o_addr + 16 * g, x);
+                            }
+                        }
+                        m = m_new;
+                        ms = ms_new;
+                    }
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        uint32_t h[16];
+#pragma unroll
+                        for (int k = 0; k < 16; k++) {
+                            float a = __uint_as_float(v[g][2 * k]), b = __uint_as_float(v[g][2 * k + 1]);
+                            fma_pair(a, b, scale, -ms);
+                            a = exp2_approx(a);
+                            b = exp2_approx(b);
+                            add_pair(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], a, b);
+                            h[k] = h2_as_u32(__floats2half2_rn(a, b));
+                        }
+                        tmem_st16(s_addr + 16 * g, h);
+                        if (g == 1 && !bad) {              // the product of the first 64 keys may start
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive1(&sh.p_ready[u][0]);
+                        }
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_wait_st();
+                    if (bad) {
+                        // a value that is not finite lies in the chunk and some rows do not see it: 0 times it would be
+                        // NaN, so each row adds up what it sees by itself (rare, and slow)
+                        if (c > c_first) {
+                            ok = wait.warp(&sh.o_done[u], (n_s - 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        const uint8_t *vs = slots + ((it0 + v_item(c, n_c, two)) % NS) * CA_SLOT;
+#pragma unroll 1
+                        for (int g = 0; g < 8; g++) {
+                            uint32_t x[16];
+                            tmem_ld16(o_addr + 16 * g, x);
+                            if (c == c_first)
+#pragma unroll
+                                for (int k = 0; k < 16; k++) x[k] = 0u;
+#pragma unroll 1
+                            for (int j = 0; j < CA_KEYS; j++) {
+                                const float2 pp = __half22float2(u32_as_h2(tmem_ld1(s_addr + (j >> 1))));
+                                const float pj = j & 1 ? pp.y : pp.x;
+                                const bool sees = j >= lo && j < hi;
+#pragma unroll
+                                for (int k = 0; k < 16; k++)
+                                    x[k] = sees ? __float_as_uint(fmaf(pj, v_at(vs, j, 16 * g + k), __uint_as_float(x[k]))) : x[k];
+                            }
+                            tmem_st16(o_addr + 16 * g, x);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive1(&sh.p_ready[u][0]);
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive1(&sh.p_ready[u][0]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&sh.p_ready[t]);
+                if (lane == 0) mbar_arrive1(&sh.p_ready[u][1]);
             }
             if (!ok) break;
-            ok = wait.warp(&sh.o_done[t], (n_s - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const bool whole = s.begins && s.ends;
-            float *part = part_row(p.ws, cta, s.begins ? 1 : 0, my);
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (!whole && valid) *reinterpret_cast<float2 *>(part) = make_float2(m == -INFINITY ? m : msc, l);
+            const bool join = !two && n_c > 1;             // both buffers hold a part of the one tile
+            if (act && c_first < n_c) {
+                ok = wait.warp(&sh.o_done[u], (n_s - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                float f0 = 1.0f, f1 = 0.0f;
+                if (join && u == 1) {
+                    sh.odd[row] = make_float2(m == -INFINITY ? m : ms, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive1(&sh.odd_full[w4]);
+                    ok = wait.warp(&sh.odd_read[w4], n_odd & 1);
+                    if (!ok) break;
+                } else {
+                    float mf = m == -INFINITY ? m : ms;
+                    if (join) {
+                        ok = wait.warp(&sh.odd_full[w4], n_odd & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float2 o = sh.odd[row];
+                        const float top = fmaxf(mf, o.x);
+                        f0 = mf == -INFINITY ? 0.0f : exp2f(mf - top);
+                        f1 = o.x == -INFINITY ? 0.0f : exp2f(o.x - top);
+                        l = f0 * l + f1 * o.y;
+                        mf = top;
+                    }
+                    const bool whole = s.begins && s.ends, valid = first + row < rows;
+                    float *part = part_row(p.ws, cta, s.begins ? 1 : 0, first + row);
+                    uint16_t *out = p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    if (!whole && valid) *reinterpret_cast<float2 *>(part) = make_float2(mf, l);
 #pragma unroll 1
-            for (int g = 0; g < 4; g++) {
-                __syncwarp();
-                uint32_t x[32];
-                tmem_ld32(o_addr + 32 * g, x);
-                tmem_wait_ld(x);
-                if (valid && whole) {
-                    store_o32(out + 32 * g, reinterpret_cast<const float *>(x), inv, p.io_type);
-                } else if (valid) {
+                    for (int g = 0; g < 4; g++) {
+                        __syncwarp();
+                        uint32_t x[32];
+                        tmem_ld32(o_addr + 32 * g, x);
+                        tmem_wait_ld(x);
+                        if (join) {
+                            uint32_t y[32];
+                            tmem_ld32(o_addr + 128 + 32 * g, y);
+                            tmem_wait_ld(y);
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        *reinterpret_cast<uint4 *>(part + 4 + 32 * g + 4 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            for (int k = 0; k < 32; k++)
+                                x[k] = __float_as_uint(fmaf(f1, __uint_as_float(y[k]), f0 * __uint_as_float(x[k])));
+                        }
+                        if (valid && whole) {
+                            store_o32(out + 32 * g, reinterpret_cast<const float *>(x), inv, p.io_type);
+                        } else if (valid) {
+#pragma unroll
+                            for (int k = 0; k < 8; k++)
+                                *reinterpret_cast<uint4 *>(part + 4 + 32 * g + 4 * k) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (join && lane == 0) mbar_arrive1(&sh.odd_read[w4]);
                 }
+                if (join) n_odd++;
             }
-            __syncwarp();
-            tc_fence_before();
-            if (s.begins && !s.ends && t == 0 && row == 0) {
+            if (s.begins && !s.ends && u == 0 && row == 0) {
                 desc->t0 = s.t0;
                 desc->h = s.h;
                 desc->row0 = s.row0;
@@ -888,6 +1001,8 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                 desc->last = s.last;
                 desc->valid = 1;
             }
+            it0 += 2 * n_c;
+            ci += n_c;
         }
     }
     tc_fence_before();
@@ -959,16 +1074,43 @@ static cudaError_t make_k_map(const ChunkAttnParams &p, CUtensorMap *map) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_chunk_attention(const ChunkAttnParams &p, cudaStream_t stream) {
-    int dev = 0, sms = 0;
+template <int ROWS, bool ALL_F16>
+constexpr int ca_smem = CaLayout<ROWS, ALL_F16>::BYTES + CA_SHARED_BYTES;
+template <int ROWS, bool ALL_F16>
+static cudaError_t allow_smem() {
+    static_assert(ca_smem<ROWS, ALL_F16> <= 232448, "shared memory of an SM");
+    return cudaFuncSetAttribute(chunk_attention_kernel<ROWS, ALL_F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, ca_smem<ROWS, ALL_F16>);
+}
+template <int ROWS, bool ALL_F16>
+static cudaError_t run(const ChunkAttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream) {
+    return launch_k(chunk_attention_kernel<ROWS, ALL_F16>, dim3(ctas), dim3(CA_THREADS), ca_smem<ROWS, ALL_F16>, false, 1, stream, p, map);
+}
+
+cudaError_t launch_chunk_attention(const ChunkAttnParams &p0, cudaStream_t stream) {
+    ChunkAttnParams p = p0;
+    // Items of 256 rows share each chunk of keys between two tiles; where requests have few tokens (as single-token
+    // steps do) most would hold one tile, whose shared memory then serves better for chunks on their way.
+    p.rows = (long long)p.T * p.G > 128LL * p.R ? 256 : 128;
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CA_SMEM);
     if (e != cudaSuccess) return e;
+    static std::atomic<int> known[64];   // SMs of a device whose kernel attributes are set
+    int sms = dev < 64 ? known[dev].load() : 0;
+    if (sms == 0) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = allow_smem<256, true>();
+        if (e == cudaSuccess) e = allow_smem<256, false>();
+        if (e == cudaSuccess) e = allow_smem<128, true>();
+        if (e == cudaSuccess) e = allow_smem<128, false>();
+        if (e != cudaSuccess) return e;
+        if (dev < 64) known[dev].store(sms);
+    }
     CUtensorMap map = {};
     if (p.kv.k_type == KV_T_F16 && (e = make_k_map(p, &map)) != cudaSuccess) return e;
     const int ctas = std::min(sms, CA_MAX_CTAS);
-    e = launch_k(chunk_attention_kernel, dim3(ctas), dim3(CA_THREADS), CA_SMEM, false, 1, stream, p, map);
+    const bool f16 = p.kv.k_type == KV_T_F16 && p.kv.v_type == KV_T_F16;
+    if (p.rows > 128) e = f16 ? run<256, true>(p, map, ctas, stream) : run<256, false>(p, map, ctas, stream);
+    else e = f16 ? run<128, true>(p, map, ctas, stream) : run<128, false>(p, map, ctas, stream);
     if (e != cudaSuccess) return e;
     return launch_k(chunk_combine_kernel, dim3(ctas, CA_COMBINE_Y), dim3(256), 0, true, 1, stream, p);
 }

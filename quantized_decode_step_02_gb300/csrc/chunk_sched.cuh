@@ -1,9 +1,9 @@
 // chunk_sched.cuh -- how the chunk attention cuts its work: host and device
 // code, exact integer arithmetic.
 //
-// A request's new tokens are taken TP at a time, TP = 256 / G tokens x G query
-// heads of one kv head = up to 256 rows: an item (request, kv head, row
-// block).  An item's keys are cut into chunks of 128 (two pages) at multiples
+// A request's new tokens are taken TP at a time, TP tokens x G query heads of
+// one kv head = up to 256 rows (128 where requests are short: the launcher's
+// choice): an item (request, kv head, row block).  An item's keys are cut into chunks of 128 (two pages) at multiples
 // of 128; its weight is its number of chunks, at least 1.  The items in order
 // (request, kv head, row block) lie on a line of W units, and CTA i of P takes
 // the units [i W / P, (i + 1) W / P): every CTA gets the same number of chunks
@@ -19,7 +19,7 @@
 
 namespace zdec {
 
-constexpr int CA_ROWS = 256, CA_KEYS = 128;   // rows of an item, keys of a chunk
+constexpr int CA_ROWS = 256, CA_KEYS = 128;   // most rows of an item, keys of a chunk
 
 // sum over i in [0, n) of floor((a i + b) / m); n, a, b >= 0, m > 0.
 ZHD long long floor_sum(long long n, long long m, long long a, long long b) {
