@@ -8,6 +8,7 @@ raises.  PyTorch is used for device buffers and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -546,24 +547,54 @@ def _tensor(x, name, dtypes, shape, device, strided=False):
         raise ZdecError(-1, f"{name} is on {x.device}, the rest on {device}")
     if not (x[:1].is_contiguous() if strided else x.is_contiguous()):
         raise ZdecError(-1, f"{name} must be contiguous" + (" within a row" if strided else ""))
-    return x
 
 
-def _call(device, stream, fn, *args):
-    """One stateless call on `device`, on `stream` (a cudaStream_t, or None: torch's current stream there)."""
-    import torch
+# The calls below are made per layer and step, so their checks come in two
+# forms: a quick one, and the one that says what is wrong.
+_I32, _I64, _U8, _HALF, _ANY = ("int32",), ("int64",), ("uint8",), ("float16", "bfloat16"), ("float32", "float16", "bfloat16")
+_DT = {}   # torch dtypes by name, and torch dtype -> zdec_float_type
+
+
+def _dtypes():
+    if not _DT:
+        import torch
+        _DT.update({n: getattr(torch, n) for n in ("int32", "int64", "uint8", "float16", "bfloat16", "float32")})
+        _DT.update({getattr(torch, n): t for n, t in _TYPE_ID.items()})
+        _DT["torch"] = torch
+    return _DT
+
+
+def _rows(x) -> int:
+    """Elements from row to row if the rows of x are contiguous within, else 0
+    (a single row's own length: its stride says nothing)."""
+    if x.is_contiguous():
+        n = x.shape[1]
+        return n * x.shape[2] if x.dim() == 3 else n
+    if x.dim() == 3:
+        ok = x.stride(2) == 1 and x.stride(1) == x.shape[2]
+        return (x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]) if ok else 0
+    return (x.stride(0) if x.shape[0] > 1 else x.shape[1]) if x.stride(1) == 1 else 0
+
+
+def _call(index, stream, fn, *args):
+    """One stateless call on CUDA device `index`, on `stream` (a cudaStream_t, or None: torch's current stream there)."""
+    torch = _dtypes()["torch"]
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
         s = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             s = fn(*args, stream)
-    _glob_check(s)
+    if s:
+        _glob_check(s)
 
 
-def _opt(x, name, dtypes, shape, device):
-    return None if x is None else _tensor(x, name, dtypes, shape, device).data_ptr()
+def _status(x, dev):
+    if x is None:
+        return None
+    _tensor(x, "status", _I32, (1,), dev)
+    return x.data_ptr()
 
 
 def chunk_plan(ctx_len, n_new, tables, cu, kv_len, positions, slots, taken, free_pages=None, stream=None):
@@ -572,23 +603,39 @@ def chunk_plan(ctx_len, n_new, tables, cu, kv_len, positions, slots, taken, free
     n_new [R], tables [R, max_pages] (entries of new pages are set when
     free_pages is given), outputs cu [R + 1], kv_len [R], positions [T], taken
     [2] and int64 slots [T].  Asynchronous."""
-    lib, dev, i32 = load_library(), getattr(ctx_len, "device", None), ("int32",)
-    _tensor(ctx_len, "ctx_len", i32, (None,), None)
-    R = ctx_len.shape[0]
-    _tensor(n_new, "n_new", i32, (R,), dev)
-    _tensor(tables, "tables", i32, (R, None), dev)
-    _tensor(cu, "cu", i32, (R + 1,), dev)
-    _tensor(kv_len, "kv_len", i32, (R,), dev)
-    _tensor(positions, "positions", i32, (None,), dev)
-    T = positions.shape[0]
-    _tensor(slots, "slots", ("int64",), (T,), dev)
-    _tensor(taken, "taken", i32, (2,), dev)
-    free = _opt(free_pages, "free_pages", i32, (None,), dev)
-    if free_pages is not None and free_pages.numel() == 0:
-        free = taken.data_ptr()   # an empty list: never read, but not "no list"
-    _call(dev, stream, lib.zdec_chunk_plan, R, ctx_len.data_ptr(), n_new.data_ptr(), free,
-          0 if free_pages is None else free_pages.numel(), tables.data_ptr(), tables.shape[1], T, cu.data_ptr(),
-          kv_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), taken.data_ptr())
+    dt = _dtypes()
+    i32 = dt["int32"]
+    ints = (ctx_len, n_new, tables, cu, kv_len, positions, taken)
+    quick = False
+    if all(getattr(x, "dtype", None) is i32 for x in ints) and getattr(slots, "dtype", None) is dt["int64"]:
+        R, T, idx = ctx_len.numel(), positions.numel(), ctx_len.get_device()
+        quick = (idx >= 0 and all(x.get_device() == idx and x.is_contiguous() for x in ints) and slots.get_device() == idx
+                 and slots.is_contiguous() and ctx_len.dim() == 1 and n_new.shape == (R,) and kv_len.shape == (R,)
+                 and cu.shape == (R + 1,) and tables.dim() == 2 and tables.shape[0] == R and positions.dim() == 1
+                 and slots.shape == (T,) and taken.shape == (2,))
+    if not quick:
+        _tensor(ctx_len, "ctx_len", _I32, (None,), None)
+        dev, R = ctx_len.device, ctx_len.shape[0]
+        _tensor(positions, "positions", _I32, (None,), dev)
+        T, idx = positions.shape[0], dev.index
+        for x, name, shape in ((n_new, "n_new", (R,)), (tables, "tables", (R, None)), (cu, "cu", (R + 1,)), (kv_len, "kv_len", (R,)),
+                               (taken, "taken", (2,))):
+            _tensor(x, name, _I32, shape, dev)
+        _tensor(slots, "slots", _I64, (T,), dev)
+    free, n_free = None, 0
+    if free_pages is not None:
+        _tensor(free_pages, "free_pages", _I32, (None,), ctx_len.device)
+        n_free = free_pages.numel()
+        free = free_pages.data_ptr() if n_free else taken.data_ptr()   # an empty list: never read, but not "no list"
+    _call(idx, stream, load_library().zdec_chunk_plan, R, ctx_len.data_ptr(), n_new.data_ptr(), free, n_free, tables.data_ptr(),
+          tables.shape[1], T, cu.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), taken.data_ptr())
+
+
+@functools.lru_cache(maxsize=64)
+def _rope(theta: float, sections: tuple):
+    if not 1 <= len(sections) <= 4:
+        raise ZdecError(-1, "sections must have 1 to 4 entries")
+    return ctypes.byref(_Rope(theta, len(sections), (ctypes.c_int * 4)(*sections)))
 
 
 def chunk_append(cache: KVPool, layer: int, qkv, positions, slots, q_out=None, rope_theta: float = 1e6,
@@ -600,41 +647,47 @@ def chunk_append(cache: KVPool, layer: int, qkv, positions, slots, q_out=None, r
     q_out [T, n_q, 128] fp16 or bf16 (or None: qkv holds no queries); sections:
     rotary pairs per position axis (sum 64); rope_theta 0: no rotation;
     status: optional int32 [1].  Asynchronous."""
-    lib, dev, nkv = load_library(), cache.device, cache.n_kv_heads
-    _tensor(qkv, "qkv", ("float32", "float16", "bfloat16"), (None, None), dev, strided=True)
-    T, width = qkv.shape
-    nq = 0 if q_out is None else q_out.shape[1] if q_out.dim() == 3 else -1
-    if width != (nq + 2 * nkv) * 128:
-        raise ZdecError(-1, f"qkv rows of {width} elements do not hold {nq} query and 2 * {nkv} K/V heads of 128")
-    if q_out is not None:
-        _tensor(q_out, "q_out", ("float16", "bfloat16"), (T, nq, 128), dev, strided=True)
-    axes = len(sections)
-    if not 1 <= axes <= 4:
-        raise ZdecError(-1, "sections must have 1 to 4 entries")
-    _tensor(positions, "positions", ("int32",), (T,) if positions.dim() == 1 and axes == 1 else (axes, T), dev)
-    _tensor(slots, "slots", ("int64",), (T,), dev)
-    rope = _Rope(rope_theta, axes, (ctypes.c_int * 4)(*sections))
-    _call(dev, stream, lib.zdec_chunk_append, cache._ref, layer, ctypes.byref(rope), T, nq, qkv.data_ptr(),
-          _TYPE_ID[str(qkv.dtype)[6:]], _row(qkv), positions.data_ptr(), slots.data_ptr(),
-          None if q_out is None else q_out.data_ptr(), F16 if q_out is None else _TYPE_ID[str(q_out.dtype)[6:]],
-          0 if q_out is None else _row(q_out), _opt(status, "status", ("int32",), (1,), dev))
-
-
-def _row(x) -> int:
-    """Elements from row to row (a single row's own length: its stride says nothing)."""
-    return x.stride(0) if x.shape[0] > 1 else x[:1].numel()
+    dt, dev, nkv, axes = _dtypes(), cache.device, cache.n_kv_heads, len(sections)
+    rope = _rope(float(rope_theta), tuple(sections))
+    idx = dev.index
+    quick = False
+    if getattr(qkv, "dtype", None) in dt and qkv.dim() == 2 and qkv.get_device() == idx:
+        T, width = qkv.shape
+        nq = 0 if q_out is None else width // 128 - 2 * nkv
+        ld, q_ld = _rows(qkv), 0 if q_out is None else _rows(q_out)
+        quick = (width == (nq + 2 * nkv) * 128 and ld > 0 and positions.dtype is dt["int32"] and slots.dtype is dt["int64"]
+                 and positions.get_device() == idx and slots.get_device() == idx and positions.is_contiguous()
+                 and slots.is_contiguous() and slots.shape == (T,) and (positions.shape == (axes, T) or (axes == 1 and positions.shape == (T,)))
+                 and (q_out is None or (q_ld > 0 and q_out.shape == (T, nq, 128) and q_out.get_device() == idx
+                                        and (q_out.dtype is dt["float16"] or q_out.dtype is dt["bfloat16"]))))
+    if not quick:
+        _tensor(qkv, "qkv", _ANY, (None, None), dev, strided=True)
+        T, width = qkv.shape
+        nq = 0 if q_out is None else q_out.shape[1] if q_out.dim() == 3 else -1
+        if width != (nq + 2 * nkv) * 128:
+            raise ZdecError(-1, f"qkv rows of {width} elements do not hold {nq} query and 2 * {nkv} K/V heads of 128")
+        if q_out is not None:
+            _tensor(q_out, "q_out", _HALF, (T, nq, 128), dev, strided=True)
+        _tensor(positions, "positions", _I32, (T,) if positions.dim() == 1 and axes == 1 else (axes, T), dev)
+        _tensor(slots, "slots", _I64, (T,), dev)
+        ld, q_ld = _rows(qkv), 0 if q_out is None else _rows(q_out)
+    _call(idx, stream, load_library().zdec_chunk_append, cache._ref, layer, rope, T, nq, qkv.data_ptr(), dt[qkv.dtype], ld,
+          positions.data_ptr(), slots.data_ptr(), None if q_out is None else q_out.data_ptr(),
+          F16 if q_out is None else dt[q_out.dtype], q_ld, _status(status, dev))
 
 
 def chunk_read(cache: KVPool, layer: int, slots, k, v, status=None, stream=None):
     """K and V of the given slots [T] int64 as fp16 rows k, v [T, n_kv, 128]
     (zdec_chunk_read); negative slots read as 0.  Asynchronous."""
-    lib, dev = load_library(), cache.device
-    _tensor(slots, "slots", ("int64",), (None,), dev)
-    T = slots.shape[0]
-    _tensor(k, "k", ("float16",), (T, cache.n_kv_heads, 128), dev)
-    _tensor(v, "v", ("float16",), (T, cache.n_kv_heads, 128), dev)
-    _call(dev, stream, lib.zdec_chunk_read, cache._ref, layer, T, slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-          _opt(status, "status", ("int32",), (1,), dev))
+    dt, dev = _dtypes(), cache.device
+    idx, want = dev.index, (getattr(slots, "shape", (0,))[0], cache.n_kv_heads, 128)
+    if not (getattr(slots, "dtype", None) is dt["int64"] and slots.dim() == 1 and slots.get_device() == idx and slots.is_contiguous()
+            and all(x.dtype is dt["float16"] and x.shape == want and x.get_device() == idx and x.is_contiguous() for x in (k, v))):
+        _tensor(slots, "slots", _I64, (None,), dev)
+        _tensor(k, "k", _HALF[:1], want, dev)
+        _tensor(v, "v", _HALF[:1], want, dev)
+    _call(idx, stream, load_library().zdec_chunk_read, cache._ref, layer, want[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _status(status, dev))
 
 
 def chunk_attention_workspace_bytes(n_q: int, n_kv_heads: int) -> int:
@@ -648,17 +701,26 @@ def chunk_attention(cache: KVPool, layer: int, q, o, cu, kv_len, tables, workspa
     strided), int32 cu [R + 1], kv_len [R], tables [R, max_pages]; workspace:
     uint8 CUDA tensor of chunk_attention_workspace_bytes(n_q, n_kv) bytes, one
     per stream of calls; scale: 1 / sqrt(128) if None.  Asynchronous."""
-    lib, dev = load_library(), cache.device
-    _tensor(q, "q", ("float16", "bfloat16"), (None, None, 128), dev, strided=True)
-    T, nq = q.shape[0], q.shape[1]
-    _tensor(o, "o", (str(q.dtype)[6:],), (T, nq, 128), dev, strided=True)
-    _tensor(kv_len, "kv_len", ("int32",), (None,), dev)
-    R = kv_len.shape[0]
-    _tensor(cu, "cu", ("int32",), (R + 1,), dev)
-    _tensor(tables, "tables", ("int32",), (R, None), dev)
-    _tensor(workspace, "workspace", ("uint8",), (None,), dev)
-    a = _ChunkAttn(nq, R, T, tables.shape[1], _TYPE_ID[str(q.dtype)[6:]], 1 if causal else 0, window,
-                   128 ** -0.5 if scale is None else scale, _row(q), _row(o))
-    _call(dev, stream, lib.zdec_chunk_attention, cache._ref, layer, ctypes.byref(a), cu.data_ptr(), kv_len.data_ptr(),
-          tables.data_ptr(), q.data_ptr(), o.data_ptr(), workspace.data_ptr(), workspace.numel(),
-          _opt(status, "status", ("int32",), (1,), dev))
+    dt, dev = _dtypes(), cache.device
+    idx, i32 = dev.index, dt["int32"]
+    quick = False
+    if (getattr(q, "dtype", None) is dt["float16"] or getattr(q, "dtype", None) is dt["bfloat16"]) and q.dim() == 3 and o.dim() == 3:
+        R, q_ld, o_ld = kv_len.numel(), _rows(q), _rows(o)
+        quick = (q.get_device() == idx and o.get_device() == idx and o.dtype is q.dtype and o.shape == q.shape and q.shape[2] == 128
+                 and q_ld > 0 and o_ld > 0
+                 and all(x.dtype is i32 and x.get_device() == idx and x.is_contiguous() for x in (cu, kv_len, tables))
+                 and kv_len.dim() == 1 and cu.shape == (R + 1,) and tables.dim() == 2 and tables.shape[0] == R
+                 and workspace.dtype is dt["uint8"] and workspace.get_device() == idx and workspace.is_contiguous())
+    if not quick:
+        _tensor(q, "q", _HALF, (None, None, 128), dev, strided=True)
+        _tensor(o, "o", (str(q.dtype)[6:],), tuple(q.shape), dev, strided=True)
+        _tensor(kv_len, "kv_len", _I32, (None,), dev)
+        R = kv_len.shape[0]
+        _tensor(cu, "cu", _I32, (R + 1,), dev)
+        _tensor(tables, "tables", _I32, (R, None), dev)
+        _tensor(workspace, "workspace", _U8, (None,), dev)
+        q_ld, o_ld = _rows(q), _rows(o)
+    T, nq, _ = q.shape
+    a = _ChunkAttn(nq, R, T, tables.shape[1], dt[q.dtype], 1 if causal else 0, window, 128 ** -0.5 if scale is None else scale, q_ld, o_ld)
+    _call(idx, stream, load_library().zdec_chunk_attention, cache._ref, layer, ctypes.byref(a), cu.data_ptr(), kv_len.data_ptr(),
+          tables.data_ptr(), q.data_ptr(), o.data_ptr(), workspace.data_ptr(), workspace.numel(), _status(status, dev))

@@ -53,10 +53,9 @@ struct CaLayout {
     static constexpr int RAWS = ALL_F16 ? 0 : (ROWS > 128 ? 6 : 7);
     static constexpr int BYTES = Q_BYTES + SLOTS * CA_SLOT + RAWS * CA_RAW;
 };
-constexpr long long CA_WAIT_LIMIT = 1LL << 32;     // clock cycles (~2 s)
+constexpr uint32_t CA_WAIT_LIMIT = 1u << 31;       // clock cycles (~1 s)
 constexpr float CA_LAG = 8.0f;                     // log2 units that m may lag behind the maximum
 constexpr int PART_LD = HD + 4;                    // floats of a partial row: m, l, -, -, o[128]
-constexpr int CA_COMBINE_Y = 8;
 constexpr int CA_SEGS = 4, CA_SEG_READERS = 14;   // segments on their way; warps that read each
 
 // Workspace: one descriptor per CTA, then two partial items per CTA (0: the
@@ -160,15 +159,27 @@ __device__ __forceinline__ bool partly_seen(const Seen &k, long long key0) {
 }
 
 // ---------------------------------------------------------------- shared ---
+constexpr int CA_BARS_1 = 2 * CA_MAX_SLOTS + CA_MAX_RAW + 5 + 8 + CA_SEGS, CA_BARS_4 = CA_MAX_SLOTS + CA_MAX_RAW + 6;
+constexpr int CA_BARS = CA_BARS_1 + CA_BARS_4 + CA_SEGS;
+__device__ __forceinline__ int bar_count(int i) { return i < CA_BARS_1 ? 1 : (i < CA_BARS_1 + CA_BARS_4 ? 4 : CA_SEG_READERS); }
 struct CaShared {
     float2 odd[128];               // (m, l) of each row over the odd chunks of an item with one tile
-    uint64_t full[CA_MAX_SLOTS], ready[CA_MAX_SLOTS], empty[CA_MAX_SLOTS];
-    uint64_t raw_full[CA_MAX_RAW], raw_empty[CA_MAX_RAW];
-    uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;   // p_ready: keys 0-63, 64-127
-    uint64_t odd_full[4], odd_read[4];   // per softmax warp: `odd` written, and O of the odd chunks read
-    uint64_t seg_full[CA_SEGS], seg_empty[CA_SEGS];
+    union {
+        uint64_t bars[CA_BARS];
+        struct {
+            // one arrival each
+            uint64_t full[CA_MAX_SLOTS], empty[CA_MAX_SLOTS], raw_full[CA_MAX_RAW], s_full[2], o_done[2], drain;
+            uint64_t odd_full[4], odd_read[4];   // per softmax warp: `odd` written, and O of the odd chunks read
+            uint64_t seg_full[CA_SEGS];
+            // four warps
+            uint64_t ready[CA_MAX_SLOTS], raw_empty[CA_MAX_RAW], q_ready[2], p_ready[2][2];   // p_ready: keys 0-63, 64-127
+            uint64_t seg_empty[CA_SEGS];
+        };
+    };
     Segment seg[CA_SEGS];
-    Walk walk;
+    ChunkReq w_q;             // the request that holds this CTA's first unit, its index, its weight per kv head,
+    int w_r;                  // and which of its units that is
+    long long w_per, w_x;
     long long scan[CA_THREADS / 32];
     uint32_t tmem;
     int abort;
@@ -194,21 +205,21 @@ __device__ __forceinline__ void item_at(int i, int n_c, bool two, int &kv, int &
     }
 }
 
+// Bounded waits (the 32-bit clock wraps after about 2 s; the bound is half of that).
 struct Waiter {
     volatile int *abort;
     uint32_t *status;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
         if (mbar_try_wait(bar, parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity)) {
-            if (*abort) return false;
-            if (clock64() - t0 > CA_WAIT_LIMIT) {
-                *abort = 1;
-                if (status) atomicOr(status, (uint32_t)ZDEC_CHUNK_TIMEOUT);
-                return false;
-            }
-        }
-        return true;
+        const uint32_t t0 = (uint32_t)clock();
+        bool late = false;
+        do {
+            if (mbar_try_wait(bar, parity)) return true;
+            late = (uint32_t)clock() - t0 > CA_WAIT_LIMIT;
+        } while (!late && !*abort);
+        *abort = 1;
+        if (late && status) atomicOr(status, (uint32_t)ZDEC_CHUNK_TIMEOUT);
+        return false;
     }
     // the same answer on every lane of a warp
     __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
@@ -324,63 +335,117 @@ __device__ __forceinline__ void prepare_v(const uint8_t *reg, uint8_t *slot, int
 }
 // V values outside tokens [lo, hi) of the chunk, or of a missing page, to 0.
 __device__ __forceinline__ void clean_v(uint8_t *slot, int d, int lo, int hi, int pages_ok) {
-    for (int u = 0; u < 4; u++) {
-        const bool there = (pages_ok >> (u >> 1)) & 1;
-        if (there && 32 * u >= lo && 32 * u + 32 <= hi) continue;
-        for (int g = 0; g < 4; g++) {
-            uint4 *at = reinterpret_cast<uint4 *>(slot + u * 8192 + d * 64 + ((g ^ ((d >> 1) & 3)) << 4));
-            const int c0 = 32 * u + 8 * g;
-            *at = there ? keep8(*at, lo - c0, hi - c0) : make_uint4(0u, 0u, 0u, 0u);
-        }
+    if (!(pages_ok & 1)) lo = max(lo, 64);
+    if (!(pages_ok & 2)) hi = min(hi, 64);
+#pragma unroll 1
+    for (int c0 = 0; c0 < CA_KEYS; c0 += 8) {
+        if (c0 >= lo && c0 + 8 <= hi) continue;
+        uint4 *at = reinterpret_cast<uint4 *>(slot + (c0 >> 5) * 8192 + d * 64 + ((((c0 >> 3) & 3) ^ ((d >> 1) & 3)) << 4));
+        *at = keep8(*at, lo - c0, hi - c0);
     }
 }
 
 // Whether dim d of a V operand chunk holds an infinity or a NaN.
 __device__ __forceinline__ bool v_not_finite(const uint8_t *slot, int d) {
-    bool bad = false;
-    for (int u = 0; u < 4; u++)
-        for (int g = 0; g < 4; g++) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(slot + u * 8192 + d * 64 + (g << 4));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            for (int i = 0; i < 4; i++) bad = bad || (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
-        }
-    return bad;
+    uint32_t bad = 0;   // an exponent of all ones plus one carries into the bit above it
+#pragma unroll 1
+    for (int g = 0; g < 16; g++) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(slot + (g >> 2) * 8192 + d * 64 + ((g & 3) << 4));
+        bad |= ((v.x & 0x7C007C00u) + 0x04000400u) | ((v.y & 0x7C007C00u) + 0x04000400u) | ((v.z & 0x7C007C00u) + 0x04000400u) |
+               ((v.w & 0x7C007C00u) + 0x04000400u);
+    }
+    return (bad & 0x80008000u) != 0;
 }
 __device__ __forceinline__ float v_at(const uint8_t *slot, int j, int d) {
     return __half2float(*reinterpret_cast<const __half *>(slot + (j >> 5) * 8192 + d * 64 +
                                                           ((((j & 31) >> 3) ^ ((d >> 1) & 3)) << 4) + (j & 7) * 2));
 }
 
-// The exponent taken out of a row of Q: 0 for fp16; bf16 goes into the operand
-// times 2^-e, which brings the row's largest element below fp16's top (exact
-// but for elements below 2^-28 of it).
-__device__ __forceinline__ int q_exponent(const uint4 *src, int io_type) {
-    if (io_type == ZDEC_F16) return 0;
-    uint32_t top = 0;   // largest magnitude bits
+// The 32 rows of a warp into its part of a Q operand tile, two rows of 16
+// lanes x 16 bytes at a time (`src`: this lane's row).  fp16 as it is; a bf16
+// row times 2^-e, which brings its largest element below fp16's top (exact but
+// for elements below 2^-28 of it).  Returns e of this lane's row.
+__device__ __forceinline__ int load_q(const uint16_t *src, int io_type, bool store, uint8_t *tile, int row0) {
+    const int lane = threadIdx.x & 31, c = lane & 15, up = lane >> 4;
+    int mine = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 v[8];
 #pragma unroll
-    for (int c = 0; c < 16; c++) {
-        const uint4 v = __ldg(src + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-    }
-    const int ex = (int)(top >> 7);   // biased exponent
-    return ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
-}
-__device__ __forceinline__ void store_q(const uint4 *src, int io_type, int e, uint8_t *tile, int row) {
-    const float f1 = exp2f((float)min(-e, 100)), f2 = exp2f((float)max(-e - 100, 0));   // e in [-140, 113]: 2^140 in two steps
-#pragma unroll
-    for (int c = 0; c < 16; c++) {
-        uint4 x = __ldg(src + c);
-        if (io_type != ZDEC_F16) {
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                w[i] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2));
-            x = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 8; i++) {
+            const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * (i0 + i) + up);
+            v[i] = __ldg(reinterpret_cast<const uint4 *>(from) + c);
         }
-        *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
+        uint8_t *to = tile + (c >> 3) * 16384 + (row0 + 2 * i0 + up) * 128;
+        if (io_type == ZDEC_F16) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (store) *reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4)) = v[i];
+            continue;
+        }
+#pragma unroll 1
+        for (int i = 0; i < 8; i++) {
+            uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, top = 0;   // largest magnitude bits of the row
+#pragma unroll
+            for (int k = 0; k < 7; k++) v[k] = v[k + 1];
+#pragma unroll
+            for (int k = 0; k < 4; k++) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(CAF, top, o));
+            const int ex = (int)(top >> 7);                  // biased exponent
+            const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
+            const int both = __shfl_sync(CAF, e, (lane & 1) * 16);
+            if ((lane >> 1) == i0 + i) mine = both;
+            // 2^-e, e in [-140, 113]: 2^140 in two steps
+            const float f1 = __int_as_float((127 + min(-e, 100)) << 23), f2 = __int_as_float((127 + max(-e - 100, 0)) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                w[k] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2));
+            if (store) *reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
+    return mine;
+}
+// 256 bytes of each of a warp's 32 rows, staged in shared memory in the same
+// arrangement, to `dst` (this lane's row; null: not written).
+__device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, uint8_t *dst) {
+    const int lane = threadIdx.x & 31, c = lane & 15;
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < 16; i++) {
+        const int row = row0 + 2 * i + (lane >> 4);
+        uint8_t *to = (uint8_t *)__shfl_sync(CAF, (unsigned long long)dst, 2 * i + (lane >> 4));
+        const uint4 x = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        if (to) *reinterpret_cast<uint4 *>(to + 16 * c) = x;
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void stage(uint8_t *tile, int row, int c, uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
+    *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(a, b, d, e);
+}
+__device__ __forceinline__ uint32_t pack_out(float x, float y, int io_type) {
+    if (io_type == ZDEC_F16) return h2_as_u32(__floats2half2_rn(x, y));
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+// Scores outside [lo, hi) of 32 to -inf.
+__device__ __forceinline__ void hide(uint32_t (&v)[32], int lo, int hi) {
+    const int a = max(lo, 0), b = min(hi, 32);
+    const uint32_t sees = b > a ? (0xFFFFFFFFu >> (32 - (b - a))) << a : 0u;
+    if (sees == 0xFFFFFFFFu) return;
+#pragma unroll
+    for (int k = 0; k < 32; k++)
+        if (!((sees >> k) & 1)) v[k] = 0xFF800000u;
+}
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+    float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
+#pragma unroll
+    for (int k = 2; k < 32; k += 4) {
+        a = fmaxf(fmaxf(a, __uint_as_float(v[k])), __uint_as_float(v[k + 1]));
+        if (k + 3 < 32) b = fmaxf(fmaxf(b, __uint_as_float(v[k + 2])), __uint_as_float(v[k + 3]));
+    }
+    return fmaxf(a, b);
 }
 // Two fp32 at a time.
 __device__ __forceinline__ void fma_pair(float &x, float &y, float a, float b) {   // x, y = x a + b, y a + b
@@ -391,24 +456,9 @@ __device__ __forceinline__ void add_pair(float &x, float &y, float a, float b) {
     asm("{\n .reg .b64 v, c;\n mov.b64 v, {%0, %1};\n mov.b64 c, {%2, %3};\n add.rn.f32x2 v, v, c;\n mov.b64 {%0, %1}, v;\n}"
         : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
-// 32 fp32 values of a row, times inv, as fp16 or bf16.
-__device__ __forceinline__ void store_o32(uint16_t *dst, const float *v, float inv, int io_type) {
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float x = v[8 * c + 2 * i] * inv, y = v[8 * c + 2 * i + 1] * inv;
-            if (io_type == ZDEC_F16) w[i] = h2_as_u32(__floats2half2_rn(x, y));
-            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(y), "f"(x));
-        }
-        reinterpret_cast<uint4 *>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
 // ------------------------------------------------------------------ kernel ---
-__device__ __forceinline__ long long div_small(long long a, int b) {   // a >= 0, b > 0
-    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+__device__ __noinline__ long long div_any(long long a, long long b) {   // a >= 0, b > 0
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 template <int ROWS, bool ALL_F16>
@@ -424,100 +474,76 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
     CaShared &sh = *reinterpret_cast<CaShared *>(dyn + Lay::BYTES);
     CaDesc *desc = reinterpret_cast<CaDesc *>(p.ws) + cta;
 
-    // ---- this CTA's piece of the line
+    // ---- this CTA's piece of the line: a prefix sum over the requests' weights, 512 at a time (the last strip's
+    // weights stay in registers: with up to 512 requests they are read once)
     const int n_kv = p.kv.n_kv;
-    ChunkReq mine;
-    long long my_w = 0, W = 0;   // the weight of this thread's request of the last strip; all requests' together
-    for (int r = tid; r < p.R; r += CA_THREADS) {
-        mine = load_req(p, r);
-        my_w = mine.before(mine.blocks()) * n_kv;
-        W += my_w;
-    }
-    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(CAF, W, o);
-    if (lane == 0) sh.scan[warp] = W;
+    ChunkReq my_q;
+    long long W = -1, run = 0, u0 = 0, u1 = 0;
+    int P = 0;
+    if (warp == 1) tmem_alloc(&sh.tmem, 512);
+    for (int i = tid; i < CA_BARS; i += CA_THREADS) mbar_init(&sh.bars[i], bar_count(i));
     if (tid == 0) {
         desc->valid = 0;
         sh.abort = 0;
     }
-    __syncthreads();
-    W = 0;
-    for (int i = 0; i < CA_THREADS / 32; i++) W += sh.scan[i];
-    const int P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has work: pieces follow each other
-    if (cta >= P) {
-        pdl_launch_dependents();
-        return;
-    }
-    const long long u0 = div_small(W * cta, P), u1 = div_small(W * (cta + 1), P);
-    if (warp == 1) tmem_alloc(&sh.tmem, 512);
-    if (tid == 0) {
-        for (int i = 0; i < 4; i++) {
-            mbar_init(&sh.odd_full[i], 1);
-            mbar_init(&sh.odd_read[i], 1);
-        }
-        for (int i = 0; i < CA_MAX_SLOTS; i++) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.ready[i], 4);
-            mbar_init(&sh.empty[i], 1);
-        }
-        for (uint32_t i = 0; i < NR; i++) {
-            mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], 4);
-        }
-        for (int t = 0; t < 2; t++) {
-            mbar_init(&sh.q_ready[t], 4);
-            mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_ready[t][0], 4);
-            mbar_init(&sh.p_ready[t][1], 4);
-            mbar_init(&sh.o_done[t], 1);
-        }
-        mbar_init(&sh.drain, 1);
-        for (int i = 0; i < CA_SEGS; i++) {
-            mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], CA_SEG_READERS);
-        }
-        mbar_fence_init();
-    }
-    __syncthreads();   // the sums above have been read
-    long long base = 0;
-    for (int r0 = 0; r0 < p.R; r0 += CA_THREADS) {
-        if (p.R > CA_THREADS) {
-            my_w = 0;
-            if (r0 + tid < p.R) {
-                mine = load_req(p, r0 + tid);
-                my_w = mine.before(mine.blocks()) * n_kv;
-            }
+    mbar_fence_init();
+    tc_fence_before();
+#pragma unroll 1
+    for (int r0 = 0;;) {
+        long long my_per = 0, my_w = 0;
+        if (r0 + tid < p.R) {
+            my_q = load_req(p, r0 + tid);
+            my_per = my_q.before(my_q.blocks());
+            my_w = my_per * n_kv;
         }
         long long incl = my_w;
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(CAF, incl, o);
             if (lane >= o) incl += v;
         }
         if (lane == 31) sh.scan[warp] = incl;
         __syncthreads();
-        long long excl = base + incl - my_w;
+        const long long base = run;
+#pragma unroll 1
         for (int i = 0; i < CA_THREADS / 32; i++) {
             const long long v = sh.scan[i];
-            if (i < warp) excl += v;
-            base += v;
-        }
-        if (my_w > 0 && excl <= u0 && u0 < excl + my_w) {
-            const long long per = div_small(my_w, n_kv), x = u0 - excl;
-            Walk w;
-            w.q = mine;
-            w.r = r0 + tid;
-            w.J = mine.blocks();
-            w.h = (int)((x >> 32) == 0 && (per >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)per) : x / per);
-            w.j = mine.block_at(x - w.h * per);
-            w.off = (int)(x - w.h * per - mine.before(w.j));
-            w.left = u1 - u0;
-            sh.walk = w;
+            if (i < warp) incl += v;
+            run += v;
         }
         __syncthreads();
-        if (base > u0) break;
+        if (W < 0) {                               // first time: up to all requests' weight
+            r0 += CA_THREADS;
+            if (r0 < p.R) continue;
+            W = run;
+            P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has work: pieces follow each other
+            if (cta >= P) break;
+            u0 = div_any(W * cta, P);
+            u1 = div_any(W * (cta + 1), P);
+            if (p.R > CA_THREADS) {                // second time: up to this CTA's first unit
+                r0 = 0;
+                run = 0;
+                continue;
+            }
+            r0 = 0;
+        }
+        const long long excl = base + incl - my_w;
+        if (my_w > 0 && excl <= u0 && u0 < excl + my_w) {
+            sh.w_q = my_q;
+            sh.w_r = r0 + tid;
+            sh.w_per = my_per;
+            sh.w_x = u0 - excl;
+        }
+        if (run > u0) break;
+        r0 += CA_THREADS;
     }
-    tc_fence_before();
-    __syncthreads();
     tc_fence_after();
+    if (cta >= P) {
+        if (warp == 1) tmem_dealloc(sh.tmem, 512);
+        pdl_launch_dependents();
+        return;
+    }
+    __syncthreads();
     const uint32_t tmem = __shfl_sync(CAF, sh.tmem, 0);
     pdl_launch_dependents();
 
@@ -534,9 +560,9 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
         si++;
     };
 
-    // registers: 4 warpgroups x 128 at launch = 64 + 80 + 2 x 184
+    // registers: 4 warpgroups x 128 at launch = 64 + 80 (or 56 + 88) + 2 x 184
     if (group == 0) {
-    reg_dec<64>();
+    reg_dec<ALL_F16 ? 64 : 56>();
     if (warp == 0) {
         // ---------------------------------------------------------- copies ---
         const uint32_t kb = kv_region_bytes(p.kv.k_type), vb = kv_region_bytes(p.kv.v_type);
@@ -579,6 +605,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                             dir++;
                             if (okm) mbar_expect_tx(bar, __popc(okm) * bytes);
                             else mbar_arrive1(bar);
+#pragma unroll 1
                             for (int k = 0; k < 2; k++) {
                                 if (!((okm >> k) & 1)) continue;
                                 const int page = k ? pb : pa;
@@ -589,6 +616,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                             }
                         }
                     } else {
+#pragma unroll 1
                         for (int k = 0; ok && k < 2; k++) {
                             const uint32_t sl = raw % NR;
                             ok = raw < NR || wait(&sh.raw_empty[sl], (raw / NR - 1) & 1);
@@ -613,11 +641,11 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
         }
         // copies in flight land before the CTA leaves, also where a wait gave up
         if (lane == 0 && sh.abort) {
-            const long long t0 = clock64();
+            const uint32_t t0 = (uint32_t)clock();
             for (uint32_t i = dir > CA_MAX_SLOTS ? dir - CA_MAX_SLOTS : 0; i < dir; i++)
-                while (!mbar_try_wait(&sh.full[i % CA_MAX_SLOTS], (i / CA_MAX_SLOTS) & 1) && clock64() - t0 < CA_WAIT_LIMIT) {}
+                while (!mbar_try_wait(&sh.full[i % CA_MAX_SLOTS], (i / CA_MAX_SLOTS) & 1) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
             for (uint32_t i = raw > NR ? raw - NR : 0; !ALL_F16 && i < raw; i++)
-                while (!mbar_try_wait(&sh.raw_full[i % NR], (i / NR) & 1) && clock64() - t0 < CA_WAIT_LIMIT) {}
+                while (!mbar_try_wait(&sh.raw_full[i % NR], (i / NR) & 1) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA ---
@@ -636,67 +664,86 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                 mbar_arrive1(&sh.seg_empty[si % CA_SEGS]);
                 if (n_c == 0) continue;
                 const int steps = two ? 2 * n_c : n_c;
-                // S of step i: chunk i / 2 of tile i % 2, or chunk i of the one tile, in buffer i % 2
-                auto qk = [&](int i) {
-                    const int u = i & 1;
-                    const uint32_t item = it0 + k_item(two ? i >> 1 : i, two);
-                    if (!two || u == 0) ok = ok && ready(item);
-                    if (!ok) return;
-                    tc_fence_after();
-                    tc_fence_order();   // S overwrites the P that the PV before reads
-                    const uint64_t qd = q_desc + (two ? u * (32768 >> 4) : 0), kd = k_desc + (item % NS) * (CA_SLOT >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; k++) {
-                        const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                        mma_ss(tmem + u * 128, qd + o, kd + o, IDESC, k > 0);
-                    }
-                    mma_commit(&sh.s_full[u]);
-                    if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
-                };
                 for (int t = 0; t < (two ? 2 : 1); t++) ok = ok && wait(&sh.q_ready[t], segs[t]++ & 1);
-                if (ok) qk(0);
-                if (ok && steps > 1) qk(1);
-                for (int i = 0; ok && i < steps; i++) {
-                    const int u = i & 1, c = two ? i >> 1 : i;
-                    const uint32_t item = it0 + v_item(c, n_c, two);
-                    if (!two || u == 0) ok = ready(item);
-                    ok = ok && wait(&sh.p_ready[u][0], n_p[u] & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = v_desc + (item % NS) * (CA_SLOT >> 4);
-                    const uint32_t od = tmem + 256 + u * 128;
-                    // a chunk whose product the softmax threads make themselves only reports
-                    const bool bad = sh.bad[(ci + c) & 7] != 0;
-                    if (!bad)
+                // step i: chunk i / 2 of tile i % 2, or chunk i of the one tile, in buffer i % 2; its S two steps ahead
+#pragma unroll 1
+                for (int i = -2; i < steps; i++) {
+                    const int u = i & 1;
+                    if (i >= 0) {
+                        const int c = two ? i >> 1 : i;
+                        const uint32_t item = it0 + v_item(c, n_c, two);
+                        if (!two || u == 0) ok = ok && ready(item);
+                        ok = ok && wait(&sh.p_ready[u][0], n_p[u] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + (item % NS) * (CA_SLOT >> 4);
+                        const uint32_t od = tmem + 256 + u * 128;
+                        // a chunk whose product the softmax threads make themselves only reports
+                        const bool bad = sh.bad[(ci + c) & 7] != 0;
+                        if (!bad)
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, i > 1 || k > 0);
-                    ok = wait(&sh.p_ready[u][1], n_p[u] & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (!bad)
+                            for (int k = 0; k < 4; k++)    // keys 0-63
+                                mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, i > 1 || k > 0);
+                        ok = wait(&sh.p_ready[u][1], n_p[u] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (!bad)
 #pragma unroll
-                        for (int k = 4; k < 8; k++)
-                            mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, true);
-                    mma_commit(&sh.o_done[u]);
-                    if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
-                    n_p[u]++;
-                    if (i + 2 < steps) qk(i + 2);
+                            for (int k = 4; k < 8; k++)
+                                mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, true);
+                        mma_commit(&sh.o_done[u]);
+                        if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                        n_p[u]++;
+                    }
+                    if (i + 2 < steps) {
+                        const uint32_t item = it0 + k_item(two ? (i + 2) >> 1 : i + 2, two);
+                        if (!two || u == 0) ok = ok && ready(item);
+                        if (!ok) break;
+                        tc_fence_after();
+                        tc_fence_order();   // S overwrites the P that the PV before reads
+                        const uint64_t qd = q_desc + (two ? u * (32768 >> 4) : 0), kd = k_desc + (item % NS) * (CA_SLOT >> 4);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                            mma_ss(tmem + u * 128, qd + o, kd + o, IDESC, k > 0);
+                        }
+                        mma_commit(&sh.s_full[u]);
+                        if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                    }
                 }
                 it0 += 2 * n_c;
                 ci += n_c;
             }
             if (!ok) {   // a wait gave up: MMAs in flight end before the CTA leaves
                 mma_commit(&sh.drain);
-                const long long t0 = clock64();
-                while (!mbar_try_wait(&sh.drain, 0) && clock64() - t0 < CA_WAIT_LIMIT) {}
+                const uint32_t t0 = (uint32_t)clock();
+                while (!mbar_try_wait(&sh.drain, 0) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
             }
         }
         __syncwarp();
     } else if (warp == 2) {
         // --------------------------------------------------------- the walk ---
+        Walk w;
+        w.r = sh.w_r;
+        w.q = sh.w_q;
+        w.J = w.q.blocks();
+        {
+            const long long x = sh.w_x, per = sh.w_per;
+            w.h = (int)div_any(x, per);
+            const long long y = x - w.h * per;
+            int a = 0, b = w.J;   // the block that holds unit y: 32 lanes try as many places at once
+            while (b - a > 1) {
+                const int step = (b - a + 31) / 32, at = a + lane * step;
+                const unsigned le = __ballot_sync(CAF, at < b && w.q.before(at) <= y);
+                const int k = 31 - __clz(le);   // lane 0 always holds
+                a += k * step;
+                b = min(b, a + step);
+            }
+            w.j = a;
+            w.off = (int)(y - (a > 0 ? w.q.before(a) : 0));
+            w.left = u1 - u0;
+        }
         if (lane == 0) {
-            Walk w = sh.walk;
             bool more = true;
             for (uint32_t i = 0; more; i++) {
                 Segment s;
@@ -710,9 +757,9 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
     }
     } else if (group == 3) {
         // ------------------------------------------------------- preparing ---
-        reg_dec<80>();
+        reg_dec<ALL_F16 ? 80 : 88>();
         const int th = tid - 384;
-        uint32_t it = 0, dir = 0, raw = 0, ci = 0;
+        uint32_t it = 0, dir = 0, raw = 0, ci = 0;   // operands, those landing as such, raw pages; chunks
         bool ok = true;
         for (; ok && next(); done()) {
             const Segment s = sh.seg[si % CA_SEGS];
@@ -721,7 +768,6 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             for (int i = 0; ok && i < 2 * s.n_c; i++, it++) {
                 int kv, c;
                 item_at(i, s.n_c, two, kv, c);
-                const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
                 const uint32_t sl = it % NS;
                 uint8_t *slot = slots + sl * CA_SLOT;
                 if (kv ? v16 : k16) {
@@ -730,6 +776,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                     dir++;
                 } else {
                     ok = it < NS || wait.warp(&sh.empty[sl], (it / NS - 1) & 1);
+#pragma unroll 1
                     for (int k = 0; ok && k < 2; k++) {
                         const uint32_t rs = raw % NR;
                         ok = wait.warp(&sh.raw_full[rs], (raw / NR) & 1);
@@ -749,6 +796,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                     if (!ok) break;
                 }
                 if (kv) {
+                    const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
                     const int lo = (int)max(0LL, seen.lo - key0), hi = (int)min((long long)CA_KEYS, seen.hi - key0);
                     const int pok = sh.pages_ok[(ci + c) & 7];
                     if (lo > 0 || hi < CA_KEYS || pok != 3) clean_v(slot, th, lo, hi, pok);
@@ -778,9 +826,8 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                 const int my = u * 128 + row;
                 if (my < rows) {
                     const int flat = s.row0 + my, tok = flat / p.G, head = s.h * p.G + flat - tok * p.G;
-                    uint16_t *out = p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD;
-                    const float zero[32] = {};
-                    for (int d = 0; d < 4; d++) store_o32(out + 32 * d, zero, 0.0f, p.io_type);
+                    uint4 *out = reinterpret_cast<uint4 *>(p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD);
+                    for (int d = 0; d < 16; d++) out[d] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 __syncwarp();
                 continue;
@@ -791,9 +838,9 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             const long long pos = s.a + tok;
             float scale = 0.0f;                            // log2 units per score
             if (act) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (long long)(s.t0 + tok) * p.q_ld + (long long)head * HD);
-                const int e = q_exponent(src, p.io_type);
-                if (two || u == 0) store_q(src, p.io_type, e, q_smem + first * 256, row);
+                const uint16_t *src = p.q + (long long)(s.t0 + tok) * p.q_ld + (long long)head * HD;
+                const bool mine = two || u == 0;
+                const int e = mine || p.io_type != ZDEC_F16 ? load_q(src, p.io_type, mine, q_smem + first * 256, w4 * 32) : 0;
                 scale = fmaxf(ldexpf(p.scale_log2, e), 7.9e-31f);   // never 0 (0 * -inf)
             }
             if (two || u == 0) {
@@ -811,9 +858,14 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                 if (!ok) break;
                 tc_fence_after();
                 if (act) {
-                    uint32_t v[4][32];
+                    // S is read once into 128 registers where the tensor core's rate counts; short items, which wait for
+                    // memory, read it twice, 64 and 32 columns at a time: a quarter of the code, fewer registers
+                    constexpr bool ONCE = ROWS > 128;
+                    uint32_t v[ONCE ? 4 : 2][32];
+                    if (ONCE) {
 #pragma unroll
-                    for (int g = 0; g < 4; g++) tmem_ld32(s_addr + 32 * g, v[g]);
+                        for (int g = 0; g < 4; g++) tmem_ld32(s_addr + 32 * g, v[ONCE ? g : 0]);
+                    }
                     const int pok = sh.pages_ok[(ci + c) & 7];
                     int lo = 0, hi = CA_KEYS;              // keys of the chunk that this row sees
                     uint32_t bad = 0;
@@ -831,25 +883,33 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                             bad = sh.bad[(ci + c) & 7];
                         }
                     }
+                    if (ONCE) {
 #pragma unroll
-                    for (int g = 0; g < 4; g++) tmem_wait_ld(v[g]);
+                        for (int g = 0; g < 4; g++) tmem_wait_ld(v[ONCE ? g : 0]);
+                    }
                     if (!ok) break;
-                    if (edge) {
+                    float top = -INFINITY;
+                    if (ONCE) {
+                        if (edge) {
 #pragma unroll
-                        for (int g = 0; g < 4; g++)
-#pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                if (32 * g + k < lo || 32 * g + k >= hi) v[g][k] = 0xFF800000u;   // -inf
+                            for (int g = 0; g < 4; g++) hide(v[ONCE ? g : 0], lo - 32 * g, hi - 32 * g);
+                        }
+                        const float a = max32(v[0]), b = max32(v[1]);
+                        top = fmaxf(fmaxf(a, b), fmaxf(max32(v[ONCE ? 2 : 0]), max32(v[ONCE ? 3 : 0])));
+                    } else {
+#pragma unroll 1
+                        for (int g = 0; g < 4; g += 2) {
+                            tmem_ld32(s_addr + 32 * g, v[0]);
+                            tmem_ld32(s_addr + 32 * g + 32, v[1]);
+                            tmem_wait_ld(v[0]);
+                            tmem_wait_ld(v[1]);
+                            if (edge) {
+                                hide(v[0], lo - 32 * g, hi - 32 * g);
+                                hide(v[1], lo - 32 * g - 32, hi - 32 * g - 32);
+                            }
+                            top = fmaxf(top, fmaxf(max32(v[0]), max32(v[1])));
+                        }
                     }
-                    float mx[4];
-#pragma unroll
-                    for (int g = 0; g < 4; g++) {
-                        mx[g] = __uint_as_float(v[g][0]);
-#pragma unroll
-                        for (int k = 1; k < 31; k += 2) mx[g] = fmaxf(fmaxf(mx[g], __uint_as_float(v[g][k])), __uint_as_float(v[g][k + 1]));
-                        mx[g] = fmaxf(mx[g], __uint_as_float(v[g][31]));
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const bool grow = (top - m) * scale > CA_LAG || (m == -INFINITY && top > m);
                     if (__any_sync(CAF, grow)) {
                         const float m_new = grow ? top : m, ms_new = grow ? top * scale : ms;
@@ -872,12 +932,18 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                         ms = ms_new;
                     }
                     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
+#pragma unroll(ONCE ? 4 : 1)
                     for (int g = 0; g < 4; g++) {
+                        if (!ONCE) {                       // P of this group lies over scores that have been read
+                            tmem_ld32(s_addr + 32 * g, v[0]);
+                            tmem_wait_ld(v[0]);
+                            if (edge) hide(v[0], lo - 32 * g, hi - 32 * g);
+                        }
+                        const uint32_t(&x)[32] = v[ONCE ? g : 0];
                         uint32_t h[16];
 #pragma unroll
                         for (int k = 0; k < 16; k++) {
-                            float a = __uint_as_float(v[g][2 * k]), b = __uint_as_float(v[g][2 * k + 1]);
+                            float a = __uint_as_float(x[2 * k]), b = __uint_as_float(x[2 * k + 1]);
                             fma_pair(a, b, scale, -ms);
                             a = exp2_approx(a);
                             b = exp2_approx(b);
@@ -960,32 +1026,36 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                         l = f0 * l + f1 * o.y;
                         mf = top;
                     }
+                    // rows leave through this warp's part of the Q tile, which no MMA reads any more, in whole lines
                     const bool whole = s.begins && s.ends, valid = first + row < rows;
+                    uint8_t *tile = q_smem + first * 256;
                     float *part = part_row(p.ws, cta, s.begins ? 1 : 0, first + row);
-                    uint16_t *out = p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD;
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                     if (!whole && valid) *reinterpret_cast<float2 *>(part) = make_float2(mf, l);
+                    uint8_t *dst = nullptr;
+                    if (valid) dst = whole ? (uint8_t *)(p.o + (long long)(s.t0 + tok) * p.o_ld + (long long)head * HD) : (uint8_t *)(part + 4);
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    if (whole) { f0 *= inv; f1 *= inv; }
 #pragma unroll 1
                     for (int g = 0; g < 4; g++) {
-                        __syncwarp();
-                        uint32_t x[32];
+                        uint32_t x[32], y[32];
                         tmem_ld32(o_addr + 32 * g, x);
+                        tmem_ld32(o_addr + (join ? 128 : 0) + 32 * g, y);   // x again where nothing is joined: f1 is 0 then
                         tmem_wait_ld(x);
-                        if (join) {
-                            uint32_t y[32];
-                            tmem_ld32(o_addr + 128 + 32 * g, y);
-                            tmem_wait_ld(y);
+                        tmem_wait_ld(y);
 #pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                x[k] = __float_as_uint(fmaf(f1, __uint_as_float(y[k]), f0 * __uint_as_float(x[k])));
-                        }
-                        if (valid && whole) {
-                            store_o32(out + 32 * g, reinterpret_cast<const float *>(x), inv, p.io_type);
-                        } else if (valid) {
+                        for (int k = 0; k < 32; k++)
+                            x[k] = __float_as_uint(join ? fmaf(f1, __uint_as_float(y[k]), f0 * __uint_as_float(x[k])) : f0 * __uint_as_float(x[k]));
+                        if (whole) {
+#pragma unroll
+                            for (int k = 0; k < 16; k++) x[k] = pack_out(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), p.io_type);
+#pragma unroll
+                            for (int k = 0; k < 4; k++) stage(tile, row, 4 * g + k, x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                        } else {
 #pragma unroll
                             for (int k = 0; k < 8; k++)
-                                *reinterpret_cast<uint4 *>(part + 4 + 32 * g + 4 * k) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                                stage(tile, row, 8 * (g & 1) + k, x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                         }
+                        if (whole ? g == 3 : g & 1) flush_rows(tile, w4 * 32, !dst || whole ? dst : dst + 256 * (g >> 1));
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1013,18 +1083,19 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
 
 // Joins the pieces of the item that CTA blockIdx.x began and a later one
 // ended, in key order: one warp per row, four dims per lane.
-__global__ __launch_bounds__(256) void chunk_combine_kernel(const __grid_constant__ ChunkAttnParams p) {
+__global__ __launch_bounds__(1024) void chunk_combine_kernel(const __grid_constant__ ChunkAttnParams p) {
     pdl_wait();
     const CaDesc *d = reinterpret_cast<const CaDesc *>(p.ws) + blockIdx.x;
     if (!d->valid) return;
     const int lane = threadIdx.x & 31, first = blockIdx.x, last = d->last, rows = d->rows;
-    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += CA_COMBINE_Y * 8) {
+    for (int row = threadIdx.x >> 5; row < rows; row += 32) {
         float m = -INFINITY;
+#pragma unroll 1
         for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, *part_row(p.ws, c, c == first ? 1 : 0, row));
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(CAF, m, o));
         float l = 0.0f;
         float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 2
         for (int c = first; c <= last; c++) {
             const float *r = part_row(p.ws, c, c == first ? 1 : 0, row);
             const float2 ml = *reinterpret_cast<const float2 *>(r);
@@ -1112,7 +1183,7 @@ cudaError_t launch_chunk_attention(const ChunkAttnParams &p0, cudaStream_t strea
     if (p.rows > 128) e = f16 ? run<256, true>(p, map, ctas, stream) : run<256, false>(p, map, ctas, stream);
     else e = f16 ? run<128, true>(p, map, ctas, stream) : run<128, false>(p, map, ctas, stream);
     if (e != cudaSuccess) return e;
-    return launch_k(chunk_combine_kernel, dim3(ctas, CA_COMBINE_Y), dim3(256), 0, true, 1, stream, p);
+    return launch_k(chunk_combine_kernel, dim3(ctas), dim3(1024), 0, true, 1, stream, p);
 }
 
 }  // namespace zdec

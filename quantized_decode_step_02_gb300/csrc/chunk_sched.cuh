@@ -13,25 +13,28 @@
 
 #if defined(__CUDACC__)
 #define ZHD __host__ __device__ __forceinline__
+#define ZHD_CALL __host__ __device__ __noinline__   // code that runs once is fetched once
 #else
 #define ZHD inline
+#define ZHD_CALL inline
 #endif
 
 namespace zdec {
 
 constexpr int CA_ROWS = 256, CA_KEYS = 128;   // most rows of an item, keys of a chunk
 
-// sum over i in [0, n) of floor((a i + b) / m); n, a, b >= 0, m > 0.
-ZHD long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum over i in [0, n) of floor((a i + b) / m); a n + b < 2^32, m > 0.  The
+// division steps of Euclid's algorithm on (m, a); 32-bit divisions.
+ZHD long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     long long s = 0;
     while (n > 0) {
-        if (a >= m) { s += (n - 1) * n / 2 * (a / m); a %= m; }
-        if (b >= m) { s += n * (b / m); b %= m; }
-        const long long y = a * n + b;
+        if (a >= m) { s += (long long)(n - 1) * n / 2 * (a / m); a %= m; }
+        if (b >= m) { s += (long long)n * (b / m); b %= m; }
+        const uint32_t y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
-        const long long t = m;
+        const uint32_t t = m;
         m = a;
         a = t;
     }
@@ -64,34 +67,26 @@ struct ChunkReq {
     }
     ZHD int weight(int j) const { const int c = chunks(j); return c > 0 ? c : 1; }
     // sum of the weights of blocks 0 .. j-1 (j <= blocks())
-    ZHD long long before(int j) const {
+    ZHD_CALL long long before(int j) const {
+        if (j <= 0) return 0;
         if (!causal) return (long long)j * weight(0);
         const int J = blocks();
+        if (J == 1) return weight(0);
         long long s = 0;
         int k = j;
-        if (k == J && k > 0) { s += weight(J - 1); k--; }   // the last block may be short
+        if (k == J) { s += weight(J - 1); k--; }   // the last block may be short
         // blocks whose keys end at or before 0: a + (i + 1) TP <= 0
         long long z = a < 0 ? -a / TP : 0;
         if (z > k) z = k;
         s += z;
-        s += floor_sum(k - z, 128, TP, a + (z + 1) * TP + 127);
+        if (k > z) s += floor_sum((uint32_t)(k - z), 128u, (uint32_t)TP, (uint32_t)(a + (z + 1) * TP + 127));
         if (window) {
             const long long w = window - 1 - a;             // lo(i) > 0 from i TP > w on
             long long i0 = w >= 0 ? w / TP + 1 : 0;
             if (i0 < z) i0 = z;
-            if (i0 < k) s -= floor_sum(k - i0, 128, TP, i0 * TP - w);
+            if (i0 < k) s -= floor_sum((uint32_t)(k - i0), 128u, (uint32_t)TP, (uint32_t)(i0 * TP - w));
         }
         return s;
-    }
-    // the block that holds unit x of before()'s line
-    ZHD int block_at(long long x) const {
-        int l = 0, h = blocks();
-        while (h - l > 1) {
-            const int m = (l + h) >> 1;
-            if (before(m) <= x) l = m;
-            else h = m;
-        }
-        return l;
     }
 };
 
