@@ -158,42 +158,26 @@ __device__ __forceinline__ long long checked_slot(const KvPool &p, long long slo
 }
 
 // ---------------------------------------------------------------- append ---
-template <int T>
-struct InType;
-template <>
-struct InType<ZDEC_F32> {
-    static __device__ __forceinline__ float2 load2(const void *p, long long i) {
-        return __ldg(reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i));
+// Eight consecutive elements of a row as fp32.
+template <int IN>
+__device__ __forceinline__ void load8(const void *p, long long i, float (&x)[8]) {
+    if (IN == ZDEC_F32) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        const float4 a = __ldcs(q), b = __ldcs(q + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float2 f = IN == ZDEC_F16 ? __half22float2(u32_as_h2(w[k]))
+                                            : make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            x[2 * k] = f.x;
+            x[2 * k + 1] = f.y;
+        }
     }
-    static __device__ __forceinline__ float4 load4(const void *p, long long i) {
-        return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
-    }
-};
-template <>
-struct InType<ZDEC_F16> {
-    static __device__ __forceinline__ float2 load2(const void *p, long long i) {
-        return __half22float2(u32_as_h2(__ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i))));
-    }
-    static __device__ __forceinline__ float4 load4(const void *p, long long i) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i));
-        const float2 a = __half22float2(u32_as_h2(w.x)), b = __half22float2(u32_as_h2(w.y));
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-};
-__device__ __forceinline__ float2 bf2_to_f2(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-template <>
-struct InType<ZDEC_BF16> {
-    static __device__ __forceinline__ float2 load2(const void *p, long long i) {
-        return bf2_to_f2(__ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i)));
-    }
-    static __device__ __forceinline__ float4 load4(const void *p, long long i) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i));
-        const float2 a = bf2_to_f2(w.x), b = bf2_to_f2(w.y);
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-};
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {   // nearest even, low half x
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
@@ -203,7 +187,7 @@ __device__ __forceinline__ uint32_t pack_f16(float x, float y) { return h2_as_u3
 
 // Two fp16 values -> two stored bytes (low first): e4m3, or Q8_0 codes + 128
 // of a block with fp32 scale d (0 for an all-zero block).
-__device__ __forceinline__ uint16_t fp8_pair(uint32_t h2) {
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t h2) {
     uint16_t out;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(out) : "r"(h2));
     return out;
@@ -216,200 +200,231 @@ __device__ __forceinline__ uint32_t q8_code(float x, float d) {
 // A block's scale from its amax: fp32 IEEE division (0 for an all-zero block).
 __device__ __forceinline__ float q8_scale(float amax) { return amax == 0.0f ? 0.0f : __fdiv_rn(amax, 127.0f); }
 
+// Eight fp32 in storage form: fp16 (16 bytes) or codes (8 bytes), a Q8_0
+// block's 32 dims being held by 4 neighbouring lanes.
+template <int T>
+__device__ __forceinline__ uint4 encode8(const float (&x)[8], float &scale) {
+    uint4 h = make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7]));
+    if (T == KV_T_F16) return h;
+    if (T == KV_T_FP8) return make_uint4(fp8_pair(h.x) | (fp8_pair(h.y) << 16), fp8_pair(h.z) | (fp8_pair(h.w) << 16), 0u, 0u);
+    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+    float f[8], m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 v = __half22float2(u32_as_h2(w[k]));
+        f[2 * k] = v.x;
+        f[2 * k + 1] = v.y;
+        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+    scale = q8_scale(m);
+    uint32_t c[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; k++) c[k >> 2] |= q8_code(f[k], scale) << (8 * (k & 3));
+    return make_uint4(c[0], c[1], 0u, 0u);
+}
+
 constexpr int AP_THREADS = 256, AP_WARPS = AP_THREADS / 32, AP_TILE = 64;   // AP_TILE: tokens of a value-head CTA
 
-// Rotation of the query and key heads: a warp takes tokens and a share of the
-// heads; lane l holds the pairs 2l and 2l + 1, whose angles it computes once
-// per token.
+// cos and sin of position x turns (0.64 fixed point), nearly rounded to
+// nearest: the nearest 64th of a turn from the table (hi + lo), the rest, at
+// most 2 pi / 128, by the Taylor series, joined by the addition theorems with
+// only the last sum rounded at full size (error below 2^-24.9).
+__device__ __forceinline__ float2 turn_cos_sin(unsigned long long x, const float4 *table) {
+    const unsigned long long k = (x + (1ULL << 57)) >> 58;
+    const float r = (float)(int)((long long)(x - (k << 58)) >> 27) * 4.5716142e-11f;   // 2 pi 2^-37
+    const float4 t = table[k & 63];
+    const float r2 = r * r;
+    const float s = fmaf(r * r2, fmaf(r2, 1.0f / 120.0f, -1.0f / 6.0f), r);            // sin r
+    const float c = r2 * fmaf(r2, fmaf(r2, -1.0f / 720.0f, 1.0f / 24.0f), -0.5f);      // cos r - 1
+    return make_float2(t.x + (fmaf(t.x, c, -t.y * s) + t.z), t.y + (fmaf(t.y, c, t.x * s) + t.w));
+}
+
+// Rotation of the query and key heads.  A warp takes a token's heads four at
+// a time: 8 lanes per head, lane j the pairs 8j .. 8j + 7 (dims 8j.. and
+// 64 + 8j..: 16-byte loads and stores).  The 64 angles are computed once per
+// token, two per lane, and passed through shared memory.
 template <int IN, int KT>
-__device__ __forceinline__ void append_qk(const ChunkAppendParams &p, int tile, int split, const unsigned long long *s_turn,
-                                          const uint8_t *s_axis) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int heads = p.nq + p.kv.n_kv;
-    const int h0 = (int)((long long)heads * split / p.splits), h1 = (int)((long long)heads * (split + 1) / p.splits);
-    const unsigned long long turn0 = s_turn[2 * lane], turn1 = s_turn[2 * lane + 1];
-    const int ax0 = s_axis[2 * lane], ax1 = s_axis[2 * lane + 1];
-    const int tile_tok = AP_WARPS * p.tok_warp;
+__device__ __forceinline__ void append_qk(const ChunkAppendParams &p, long long tile, int split, const unsigned long long *s_turn,
+                                          const uint8_t *s_axis, const float4 *s_table, float2 (*s_cs)[64]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 7;
+    const int heads = p.nq + p.kv.n_kv, groups = (heads + 3) / 4;
+    const int g0 = (int)((long long)groups * split / p.splits), g1 = (int)((long long)groups * (split + 1) / p.splits);
     for (int i = 0; i < p.tok_warp; i++) {
-        const long long t = (long long)tile * tile_tok + i * AP_WARPS + warp;
+        const long long t = (tile * p.tok_warp + i) * AP_WARPS + warp;
         if (t >= p.T) break;
-        float s0, c0, s1, c1;
-        {
-            const long long a = __ldg(p.positions + (size_t)ax0 * p.T + t), b = __ldg(p.positions + (size_t)ax1 * p.T + t);
-            // position * turns mod 1 in 0.64 fixed point; the signed high word is the angle in half turns / 2^31
-            const int fa = (int)(((unsigned long long)a * turn0) >> 32), fb = (int)(((unsigned long long)b * turn1) >> 32);
-            sincospif((float)fa * 4.656612873077393e-10f, &s0, &c0);
-            sincospif((float)fb * 4.656612873077393e-10f, &s1, &c1);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int pair = lane + 32 * k;
+            const long long pos = __ldg(p.positions + (size_t)s_axis[pair] * p.T + t);
+            s_cs[warp][pair] = turn_cos_sin((unsigned long long)pos * s_turn[pair], s_table);
         }
-        const long long slot = h1 > p.nq ? checked_slot(p.kv, __ldg(p.slots + t), p.status) : -1;
+        const long long slot = checked_slot(p.kv, __ldg(p.slots + t), p.status);
+        __syncwarp();
+        float2 cs[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) cs[k] = s_cs[warp][8 * j + k];
         const long long row = t * p.ld;
-#pragma unroll 4
-        for (int h = h0; h < h1; h++) {
-            const float2 a = InType<IN>::load2(p.qkv, row + (long long)h * HD + 2 * lane);
-            const float2 b = InType<IN>::load2(p.qkv, row + (long long)h * HD + 64 + 2 * lane);
-            const float x0 = a.x * c0 - b.x * s0, x1 = a.y * c1 - b.y * s1;
-            const float y0 = b.x * c0 + a.x * s0, y1 = b.y * c1 + a.y * s1;
-            if (h < p.nq) {
-                uint32_t *q = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.q_out) + t * p.q_ld + (long long)h * HD + 2 * lane);
-                q[0] = p.q_type == ZDEC_F16 ? pack_f16(x0, x1) : pack_bf16(x0, x1);
-                q[32] = p.q_type == ZDEC_F16 ? pack_f16(y0, y1) : pack_bf16(y0, y1);
-                continue;
+#pragma unroll 2
+        for (int g = g0; g < g1; g++) {
+            const int h = 4 * g + (lane >> 3), hh = min(h, heads - 1);   // lanes past the last head repeat it
+            float a[8], b[8], x[8], y[8];
+            load8<IN>(p.qkv, row + (long long)hh * HD + 8 * j, a);
+            load8<IN>(p.qkv, row + (long long)hh * HD + 64 + 8 * j, b);
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                // a c - b s and b c + a s with the second product's rounding error put back
+                const float u = b[k] * cs[k].y, v = a[k] * cs[k].y;
+                x[k] = fmaf(a[k], cs[k].x, -u) - fmaf(b[k], cs[k].y, -u);
+                y[k] = fmaf(b[k], cs[k].x, v) + fmaf(a[k], cs[k].y, -v);
             }
-            if (slot < 0) continue;   // the whole warp: one token
+            if (h < p.nq) {
+                uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + t * p.q_ld + (long long)h * HD + 8 * j);
+                if (p.q_type == ZDEC_F16) {
+                    q[0] = make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7]));
+                    q[8] = make_uint4(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
+                } else {
+                    q[0] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    q[8] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                }
+            }
+            if (4 * g + 3 < p.nq) continue;   // no key head in this group
+            float dx = 0.0f, dy = 0.0f;
+            const uint4 ex = encode8<KT>(x, dx), ey = encode8<KT>(y, dy);
+            if (slot < 0 || h < p.nq || h >= heads) continue;
             uint8_t *reg = chunk_of_page(p.kv, p.layer, h - p.nq, slot >> 6);
             const int tl = (int)(slot & 63);
-            const uint32_t hx = pack_f16(x0, x1), hy = pack_f16(y0, y1);
             if (KT == KV_T_F16) {
-                *reinterpret_cast<uint32_t *>(reg + k16_off(tl, 2 * lane)) = hx;
-                *reinterpret_cast<uint32_t *>(reg + k16_off(tl, 64 + 2 * lane)) = hy;
-            } else if (KT == KV_T_FP8) {
-                *reinterpret_cast<uint16_t *>(reg + k8_off(tl, 2 * lane)) = fp8_pair(hx);
-                *reinterpret_cast<uint16_t *>(reg + k8_off(tl, 64 + 2 * lane)) = fp8_pair(hy);
+                *reinterpret_cast<uint4 *>(reg + k16_off(tl, 8 * j)) = ex;
+                *reinterpret_cast<uint4 *>(reg + k16_off(tl, 64 + 8 * j)) = ey;
             } else {
-                // blocks of 32 dims: lanes 0-15 hold blocks 0 and 2, lanes 16-31 blocks 1 and 3
-                const float2 fx = __half22float2(u32_as_h2(hx)), fy = __half22float2(u32_as_h2(hy));
-                float mx = fmaxf(fabsf(fx.x), fabsf(fx.y)), my = fmaxf(fabsf(fy.x), fabsf(fy.y));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) {
-                    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-                    my = fmaxf(my, __shfl_xor_sync(FULL, my, o));
-                }
-                const float dx = q8_scale(mx), dy = q8_scale(my);
-                *reinterpret_cast<uint16_t *>(reg + k8_off(tl, 2 * lane)) = (uint16_t)(q8_code(fx.x, dx) | (q8_code(fx.y, dx) << 8));
-                *reinterpret_cast<uint16_t *>(reg + k8_off(tl, 64 + 2 * lane)) = (uint16_t)(q8_code(fy.x, dy) | (q8_code(fy.y, dy) << 8));
-                if ((lane & 15) == 0) {
-                    *reinterpret_cast<uint16_t *>(reg + ks_off(tl, lane >> 4)) = __half_as_ushort(__float2half_rn(dx));
-                    *reinterpret_cast<uint16_t *>(reg + ks_off(tl, 2 + (lane >> 4))) = __half_as_ushort(__float2half_rn(dy));
+                *reinterpret_cast<uint2 *>(reg + k8_off(tl, 8 * j)) = make_uint2(ex.x, ex.y);
+                *reinterpret_cast<uint2 *>(reg + k8_off(tl, 64 + 8 * j)) = make_uint2(ey.x, ey.y);
+                if (KT == KV_T_Q8 && (j & 3) == 0) {
+                    *reinterpret_cast<uint16_t *>(reg + ks_off(tl, j >> 2)) = __half_as_ushort(__float2half_rn(dx));
+                    *reinterpret_cast<uint16_t *>(reg + ks_off(tl, 2 + (j >> 2))) = __half_as_ushort(__float2half_rn(dy));
                 }
             }
         }
     }
+}
+
+// What thread `i` of a tile's tokens does with the 16-byte value segments of
+// `seg` tokens: 1 the token opens a segment that the tile fills, 0 it lies
+// inside one, 2 its element goes alone, 3 it has no slot.
+__device__ __forceinline__ uint8_t segment_role(const long long *s_slot, int i, int n, int seg) {
+    const long long slot = s_slot[i];
+    if (slot < 0) return 3;
+    const int in = (int)(slot & (seg - 1)), a = i - in;   // a: where the segment's first token would be
+    if (a < 0 || a + seg > n) return 2;
+    for (int e = 0; e < seg; e++)
+        if (s_slot[a + e] != slot - in + e) return 2;
+    return in == 0;
 }
 
 // One value head of up to AP_TILE tokens: encoded rows meet in shared memory
-// and leave transposed, 16 bytes (SEG tokens of one dim) at a time where SEG
-// tokens of the tile fill one 16-byte segment of the page, else element by
-// element.
+// and leave transposed, 16 bytes (8 or 16 tokens of one dim) at a time where
+// those tokens fill one 16-byte segment of the page, else element by element.
 template <int IN, int VT>
-__device__ __forceinline__ void append_v(const ChunkAppendParams &p, int tile, int head, uint8_t *smem, long long *s_slot) {
+__device__ __forceinline__ void append_v(const ChunkAppendParams &p, long long tile, int head, uint8_t *smem, long long *s_slot,
+                                         uint8_t *s_role) {
     constexpr int ES = VT == KV_T_F16 ? 2 : 1, SEG = 16 / ES;
-    constexpr int PITCH = HD * ES + 4;   // bytes of a row: 4 more, so that the rows of a column fall in different banks
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long t0 = (long long)tile * AP_TILE;
+    constexpr int PITCH = HD * ES + 16;   // bytes of a row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 15;
+    const long long t0 = tile * AP_TILE;
     const int n = (int)min((long long)AP_TILE, p.T - t0);
-    if ((int)threadIdx.x < AP_TILE)
-        s_slot[threadIdx.x] = (int)threadIdx.x < n ? checked_slot(p.kv, __ldg(p.slots + t0 + threadIdx.x), p.status) : -1;
+    if ((int)threadIdx.x < n) s_slot[threadIdx.x] = checked_slot(p.kv, __ldg(p.slots + t0 + threadIdx.x), p.status);
     __syncthreads();
+    if ((int)threadIdx.x < n) s_role[threadIdx.x] = segment_role(s_slot, threadIdx.x, n, SEG);
     const long long col = (long long)(p.nq + p.kv.n_kv + head) * HD;
-#pragma unroll 4
-    for (int i = warp; i < n; i += AP_WARPS) {
-        const float4 x = InType<IN>::load4(p.qkv, (t0 + i) * p.ld + col + 4 * lane);
-        const uint32_t h0 = pack_f16(x.x, x.y), h1 = pack_f16(x.z, x.w);
-        uint8_t *row = smem + i * PITCH;
-        if (VT == KV_T_F16) {
-            *reinterpret_cast<uint32_t *>(row + 8 * lane) = h0;
-            *reinterpret_cast<uint32_t *>(row + 8 * lane + 4) = h1;
-        } else if (VT == KV_T_FP8) {
-            *reinterpret_cast<uint32_t *>(row + 4 * lane) = (uint32_t)fp8_pair(h0) | ((uint32_t)fp8_pair(h1) << 16);
-        } else {
-            const float2 a = __half22float2(u32_as_h2(h0)), b = __half22float2(u32_as_h2(h1));
-            float m = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
-            m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));   // a block of 32 dims: 8 lanes
-            m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
-            m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
-            const float d = q8_scale(m);
-            *reinterpret_cast<uint32_t *>(row + 4 * lane) =
-                q8_code(a.x, d) | (q8_code(a.y, d) << 8) | (q8_code(b.x, d) << 16) | (q8_code(b.y, d) << 24);
-            const long long slot = s_slot[i];
-            if ((lane & 7) == 0 && slot >= 0) {
-                uint8_t *reg = chunk_of_page(p.kv, p.layer, head, slot >> 6) + kv_region_bytes(p.kv.k_type);
-                *reinterpret_cast<uint16_t *>(reg + vs_off((int)(slot & 63), lane >> 3)) = __half_as_ushort(__float2half_rn(d));
-            }
+#pragma unroll 2
+    for (int i0 = 2 * warp; i0 < n; i0 += 2 * AP_WARPS) {   // two tokens of 16 lanes x 8 dims
+        const int i = i0 + (lane >> 4), ii = min(i, n - 1);
+        float x[8], d = 0.0f;
+        load8<IN>(p.qkv, (t0 + ii) * p.ld + col + 8 * j, x);
+        const uint4 e = encode8<VT>(x, d);
+        if (i >= n) continue;
+        if (VT == KV_T_F16) *reinterpret_cast<uint4 *>(smem + i * PITCH + 16 * j) = e;
+        else *reinterpret_cast<uint2 *>(smem + i * PITCH + 8 * j) = make_uint2(e.x, e.y);
+        const long long slot = s_slot[i];
+        if (VT == KV_T_Q8 && (j & 3) == 0 && slot >= 0) {
+            uint8_t *reg = chunk_of_page(p.kv, p.layer, head, slot >> 6) + kv_region_bytes(p.kv.k_type);
+            *reinterpret_cast<uint16_t *>(reg + vs_off((int)(slot & 63), j >> 2)) = __half_as_ushort(__float2half_rn(d));
         }
     }
     __syncthreads();
-    // thread: dim d, tokens i = i0, i0 + 2, ...: a token that opens a whole
-    // segment stores it, one inside a whole segment does nothing
     const int d = threadIdx.x & (HD - 1);
     for (int i = threadIdx.x >> 7; i < n; i += AP_THREADS / HD) {
+        const int role = s_role[i];
+        if (role == 0 || role == 3) continue;
         const long long slot = s_slot[i];
-        if (slot < 0) continue;
-        const int in = (int)(slot & (SEG - 1)), a = i - in;   // a: where the segment's first token would be
-        bool whole = a >= 0 && a + SEG <= n;
-        if (whole)
-            for (int e = 0; e < SEG; e++) whole = whole && s_slot[a + e] == slot - in + e;
-        if (whole && in != 0) continue;
         uint8_t *reg = chunk_of_page(p.kv, p.layer, head, slot >> 6) + kv_region_bytes(p.kv.k_type);
         const int tl = (int)(slot & 63);
-        if (VT == KV_T_F16) {
-            uint8_t *dst = reg + v16_off(tl, d);
-            const uint16_t *src = reinterpret_cast<const uint16_t *>(smem + i * PITCH) + d;
-            if (whole) {
-                uint32_t w[4];
+        uint8_t *dst = reg + (VT == KV_T_F16 ? v16_off(tl, d) : v8_off(tl, d));
+        const uint8_t *src = smem + i * PITCH + d * ES;
+        if (role == 1) {
+            uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    w[e] = (uint32_t)src[(2 * e) * (PITCH / 2)] | ((uint32_t)src[(2 * e + 1) * (PITCH / 2)] << 16);
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                *reinterpret_cast<uint16_t *>(dst) = src[0];
-            }
+            for (int e = 0; e < 4; e++)
+                w[e] = ES == 2 ? (uint32_t)*reinterpret_cast<const uint16_t *>(src + (2 * e) * PITCH) |
+                                     ((uint32_t)*reinterpret_cast<const uint16_t *>(src + (2 * e + 1) * PITCH) << 16)
+                               : (uint32_t)src[(4 * e) * PITCH] | ((uint32_t)src[(4 * e + 1) * PITCH] << 8) |
+                                     ((uint32_t)src[(4 * e + 2) * PITCH] << 16) | ((uint32_t)src[(4 * e + 3) * PITCH] << 24);
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (ES == 2) {
+            *reinterpret_cast<uint16_t *>(dst) = *reinterpret_cast<const uint16_t *>(src);
         } else {
-            uint8_t *dst = reg + v8_off(tl, d);
-            const uint8_t *src = smem + i * PITCH + d;
-            if (whole) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    w[e] = (uint32_t)src[(4 * e) * PITCH] | ((uint32_t)src[(4 * e + 1) * PITCH] << 8) |
-                           ((uint32_t)src[(4 * e + 2) * PITCH] << 16) | ((uint32_t)src[(4 * e + 3) * PITCH] << 24);
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                *dst = src[0];
-            }
+            *dst = *src;
         }
     }
 }
 
-// grid (token tiles, splits + value heads): y < splits rotate, the others move values.
 template <int IN>
 __global__ __launch_bounds__(AP_THREADS) void chunk_append_kernel(const __grid_constant__ ChunkAppendParams p) {
-    __shared__ unsigned long long s_turn[64];
-    __shared__ uint8_t s_axis[64];
-    __shared__ long long s_slot[AP_TILE];
-    __shared__ __align__(16) uint8_t s_v[AP_TILE * (HD * 2 + 4)];
-    if ((int)blockIdx.y < p.splits) {
+    union Shared {
+        struct { unsigned long long turn[64]; float4 table[64]; float2 cs[AP_WARPS][64]; uint8_t axis[64]; } qk;
+        struct { uint8_t v[AP_TILE * (HD * 2 + 16)]; long long slot[AP_TILE]; uint8_t role[AP_TILE]; } v;
+    };
+    __shared__ __align__(16) Shared s;
+    if ((int)blockIdx.x < p.qk_ctas) {
         if (threadIdx.x < 64) {
-            s_turn[threadIdx.x] = p.rope.turn[threadIdx.x];
-            s_axis[threadIdx.x] = p.rope.axis[threadIdx.x];
+            s.qk.turn[threadIdx.x] = p.rope.turn[threadIdx.x];
+            s.qk.table[threadIdx.x] = p.rope.table[threadIdx.x];
+            s.qk.axis[threadIdx.x] = p.rope.axis[threadIdx.x];
         }
         __syncthreads();
-        for (long long tile = blockIdx.x; tile * AP_WARPS * p.tok_warp < p.T; tile += gridDim.x) {
-            switch (p.kv.k_type) {
-                case KV_T_F16: append_qk<IN, KV_T_F16>(p, (int)tile, blockIdx.y, s_turn, s_axis); break;
-                case KV_T_Q8: append_qk<IN, KV_T_Q8>(p, (int)tile, blockIdx.y, s_turn, s_axis); break;
-                default: append_qk<IN, KV_T_FP8>(p, (int)tile, blockIdx.y, s_turn, s_axis); break;
-            }
+        const long long tile = blockIdx.x / p.splits;
+        const int split = blockIdx.x % p.splits;
+        switch (p.kv.k_type) {
+            case KV_T_F16: append_qk<IN, KV_T_F16>(p, tile, split, s.qk.turn, s.qk.axis, s.qk.table, s.qk.cs); break;
+            case KV_T_Q8: append_qk<IN, KV_T_Q8>(p, tile, split, s.qk.turn, s.qk.axis, s.qk.table, s.qk.cs); break;
+            default: append_qk<IN, KV_T_FP8>(p, tile, split, s.qk.turn, s.qk.axis, s.qk.table, s.qk.cs); break;
         }
     } else {
-        for (long long tile = blockIdx.x; tile * AP_TILE < p.T; tile += gridDim.x) {
-            for (int head = blockIdx.y - p.splits; head < p.kv.n_kv; head += gridDim.y - p.splits) {
-                switch (p.kv.v_type) {
-                    case KV_T_F16: append_v<IN, KV_T_F16>(p, (int)tile, head, s_v, s_slot); break;
-                    case KV_T_Q8: append_v<IN, KV_T_Q8>(p, (int)tile, head, s_v, s_slot); break;
-                    default: append_v<IN, KV_T_FP8>(p, (int)tile, head, s_v, s_slot); break;
-                }
-                __syncthreads();
-            }
+        const unsigned v = blockIdx.x - p.qk_ctas;
+        const long long tile = v / p.kv.n_kv;
+        const int head = v % p.kv.n_kv;
+        switch (p.kv.v_type) {
+            case KV_T_F16: append_v<IN, KV_T_F16>(p, tile, head, s.v.v, s.v.slot, s.v.role); break;
+            case KV_T_Q8: append_v<IN, KV_T_Q8>(p, tile, head, s.v.v, s.v.slot, s.v.role); break;
+            default: append_v<IN, KV_T_FP8>(p, tile, head, s.v.v, s.v.slot, s.v.role); break;
         }
     }
 }
 
 cudaError_t launch_chunk_append(ChunkAppendParams p, cudaStream_t stream) {
-    const int heads = p.nq + p.kv.n_kv;
-    p.tok_warp = AP_TILE / AP_WARPS;
-    p.splits = std::max(1, std::min(heads, 8));
-    const long long tiles = ((long long)p.T + AP_TILE - 1) / AP_TILE;
-    const dim3 grid((unsigned)std::min(tiles, 1LL << 20), (unsigned)(p.splits + std::min(p.kv.n_kv, 4096)));
+    const int groups = (p.nq + p.kv.n_kv + 3) / 4;
+    // Few tokens: their heads are split until a wave of CTAs is full; many: a warp takes two tokens, which halves the
+    // CTAs' start (tables into shared memory).
+    p.tok_warp = p.T > 2 * 152 * AP_WARPS ? 2 : 1;
+    const long long tiles = ((long long)p.T + AP_WARPS * p.tok_warp - 1) / (AP_WARPS * p.tok_warp);
+    p.splits = (int)std::max(1LL, std::min((long long)groups, 2 * 152 / tiles));
+    const long long qk = tiles * p.splits, v = ((long long)p.T + AP_TILE - 1) / AP_TILE * p.kv.n_kv;
+    if (qk + v > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    p.qk_ctas = (int)qk;
+    const unsigned grid = (unsigned)(qk + v);
     switch (p.in_type) {
         case ZDEC_F32: chunk_append_kernel<ZDEC_F32><<<grid, AP_THREADS, 0, stream>>>(p); break;
         case ZDEC_F16: chunk_append_kernel<ZDEC_F16><<<grid, AP_THREADS, 0, stream>>>(p); break;
@@ -425,55 +440,116 @@ __device__ __forceinline__ float q8_value(float scale, uint32_t code) {
     const float x = scale * (float)((int)code - 128);
     return x > 65504.0f ? 65504.0f : (x < -65504.0f ? -65504.0f : x);
 }
-// One warp per (token, kv head), lane l: dims 4l .. 4l + 3 of K and V.
-__global__ void chunk_read_kernel(const KvPool a, int layer, int T, const int64_t *__restrict__ slots,
-                                  uint16_t *__restrict__ k, uint16_t *__restrict__ v, uint32_t *status) {
-    const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (w >= (long long)T * a.n_kv) return;
-    const long long t = w / a.n_kv;
-    const int g = (int)(w % a.n_kv);
-    const long long slot = checked_slot(a, slots[t], status);
-    uint2 ko = make_uint2(0u, 0u), vo = ko;
-    if (slot >= 0) {
-        const uint8_t *kr = chunk_of_page(a, layer, g, slot >> 6), *vr = kr + kv_region_bytes(a.k_type);
-        const int tl = (int)(slot & 63), d = 4 * lane;
-        if (a.k_type == KV_T_F16) {
-            ko = *reinterpret_cast<const uint2 *>(kr + k16_off(tl, d));
+// Eight codes -> eight fp16.
+__device__ __forceinline__ uint4 decode8(uint2 c, int type, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        if (type == KV_T_FP8) {
+            o[2 * i] = e4m3x2_to_h2((uint16_t)w[i]);
+            o[2 * i + 1] = e4m3x2_to_h2((uint16_t)(w[i] >> 16));
         } else {
-            const uint32_t c = *reinterpret_cast<const uint32_t *>(kr + k8_off(tl, d));
-            if (a.k_type == KV_T_FP8) {
-                ko = make_uint2(e4m3x2_to_h2((uint16_t)c), e4m3x2_to_h2((uint16_t)(c >> 16)));
-            } else {
-                const float s = __half2float(*reinterpret_cast<const __half *>(kr + ks_off(tl, lane >> 3)));
-                float f[4];
-                for (int e = 0; e < 4; e++) f[e] = q8_value(s, (c >> (8 * e)) & 255u);
-                ko = make_uint2(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]));
-            }
+            o[2 * i] = pack_f16(q8_value(scale, w[i] & 255u), q8_value(scale, (w[i] >> 8) & 255u));
+            o[2 * i + 1] = pack_f16(q8_value(scale, (w[i] >> 16) & 255u), q8_value(scale, w[i] >> 24));
         }
-        uint16_t e4[4];
-        float s = 1.0f;
-        if (a.v_type == KV_T_Q8) s = __half2float(*reinterpret_cast<const __half *>(vr + vs_off(tl, lane >> 3)));
-        for (int e = 0; e < 4; e++) {
-            if (a.v_type == KV_T_F16) e4[e] = *reinterpret_cast<const uint16_t *>(vr + v16_off(tl, d + e));
-            else {
-                const uint8_t c = vr[v8_off(tl, d + e)];
-                e4[e] = a.v_type == KV_T_FP8 ? (uint16_t)(e4m3x2_to_h2(c) & 0xFFFFu)
-                                             : __half_as_ushort(__float2half_rn(q8_value(s, c)));
-            }
-        }
-        vo = make_uint2((uint32_t)e4[0] | ((uint32_t)e4[1] << 16), (uint32_t)e4[2] | ((uint32_t)e4[3] << 16));
     }
-    *reinterpret_cast<uint2 *>(k + w * HD + 4 * lane) = ko;
-    *reinterpret_cast<uint2 *>(v + w * HD + 4 * lane) = vo;
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A CTA reads one kv head of up to AP_TILE slots.  K rows go straight through,
+// 16 lanes x 8 dims each; V goes through shared memory, a 16-byte segment (8
+// or 16 tokens of one dim) at a time where the tile's slots fill it.
+__global__ __launch_bounds__(AP_THREADS) void chunk_read_kernel(const __grid_constant__ KvPool a, int layer, int T,
+                                                                const int64_t *__restrict__ slots, uint16_t *__restrict__ k,
+                                                                uint16_t *__restrict__ v, uint32_t *status) {
+    constexpr int PITCH = HD * 2 + 16;
+    __shared__ __align__(16) uint8_t s_v[AP_TILE * PITCH];
+    __shared__ long long s_slot[AP_TILE];
+    __shared__ uint8_t s_role[AP_TILE];
+    __shared__ float s_scale[AP_TILE][4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 15;
+    const long long t0 = (long long)(blockIdx.x / a.n_kv) * AP_TILE;
+    const int head = blockIdx.x % a.n_kv, n = (int)min((long long)AP_TILE, T - t0);
+    const int seg = a.v_type == KV_T_F16 ? 8 : 16;
+    if ((int)threadIdx.x < n) s_slot[threadIdx.x] = checked_slot(a, __ldg(slots + t0 + threadIdx.x), status);
+    __syncthreads();
+    if ((int)threadIdx.x < n) s_role[threadIdx.x] = segment_role(s_slot, threadIdx.x, n, seg);
+    if (a.v_type == KV_T_Q8 && (int)threadIdx.x < 4 * n) {
+        const long long slot = s_slot[threadIdx.x >> 2];
+        if (slot >= 0)
+            s_scale[threadIdx.x >> 2][threadIdx.x & 3] = __half2float(*reinterpret_cast<const __half *>(
+                chunk_of_page(a, layer, head, slot >> 6) + kv_region_bytes(a.k_type) + vs_off((int)(slot & 63), threadIdx.x & 3)));
+    }
+    __syncthreads();
+    // V: thread = dim
+    const int d = threadIdx.x & (HD - 1);
+#pragma unroll 4
+    for (int i = threadIdx.x >> 7; i < n; i += AP_THREADS / HD) {
+        const int role = s_role[i];
+        uint16_t *dst = reinterpret_cast<uint16_t *>(s_v + i * PITCH) + d;
+        if (role == 0) continue;
+        if (role == 3) { *dst = 0; continue; }
+        const long long slot = s_slot[i];
+        const int tl = (int)(slot & 63);
+        const uint8_t *reg = chunk_of_page(a, layer, head, slot >> 6) + kv_region_bytes(a.k_type);
+        if (a.v_type == KV_T_F16) {
+            const uint8_t *src = reg + v16_off(tl, d);
+            if (role == 2) { *dst = *reinterpret_cast<const uint16_t *>(src); continue; }
+            const uint4 x = *reinterpret_cast<const uint4 *>(src);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 8; e++) dst[e * (PITCH / 2)] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        } else {
+            const uint8_t *src = reg + v8_off(tl, d);
+            const int m = role == 2 ? 1 : 16;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (role == 2) x.x = *src;
+            else x = *reinterpret_cast<const uint4 *>(src);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                if (e >= m) break;
+                const uint32_t c = (w[e >> 2] >> (8 * (e & 3))) & 255u;
+                dst[e * (PITCH / 2)] = a.v_type == KV_T_FP8 ? (uint16_t)(e4m3x2_to_h2((uint16_t)c) & 0xFFFFu)
+                                                            : __half_as_ushort(__float2half_rn(q8_value(s_scale[i + e][d >> 5], c)));
+            }
+        }
+    }
+    // K meanwhile: two tokens per warp
+#pragma unroll 4
+    for (int i0 = 2 * warp; i0 < n; i0 += 2 * AP_WARPS) {
+        const int i = i0 + (lane >> 4);
+        if (i >= n) continue;
+        const long long slot = s_slot[i];
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (slot >= 0) {
+            const uint8_t *reg = chunk_of_page(a, layer, head, slot >> 6);
+            const int tl = (int)(slot & 63);
+            if (a.k_type == KV_T_F16) {
+                o = *reinterpret_cast<const uint4 *>(reg + k16_off(tl, 8 * j));
+            } else {
+                const float s = a.k_type == KV_T_Q8 ? __half2float(*reinterpret_cast<const __half *>(reg + ks_off(tl, j >> 2))) : 0.0f;
+                o = decode8(*reinterpret_cast<const uint2 *>(reg + k8_off(tl, 8 * j)), a.k_type, s);
+            }
+        }
+        __stcs(reinterpret_cast<uint4 *>(k + ((t0 + i) * a.n_kv + head) * HD + 8 * j), o);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i0 = 2 * warp; i0 < n; i0 += 2 * AP_WARPS) {
+        const int i = i0 + (lane >> 4);
+        if (i < n)
+            __stcs(reinterpret_cast<uint4 *>(v + ((t0 + i) * a.n_kv + head) * HD + 8 * j),
+                   *reinterpret_cast<const uint4 *>(s_v + i * PITCH + 16 * j));
+    }
 }
 
 cudaError_t launch_chunk_read(const KvPool &kv, int layer, int T, const int64_t *slots, uint16_t *k, uint16_t *v,
                               uint32_t *status, cudaStream_t stream) {
-    const long long warps = (long long)T * kv.n_kv;
-    const long long blocks = (warps * 32 + 255) / 256;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    chunk_read_kernel<<<(unsigned)blocks, 256, 0, stream>>>(kv, layer, T, slots, k, v, status);
+    const long long ctas = ((long long)T + AP_TILE - 1) / AP_TILE * kv.n_kv;
+    if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    chunk_read_kernel<<<(unsigned)ctas, AP_THREADS, 0, stream>>>(kv, layer, T, slots, k, v, status);
     return cudaGetLastError();
 }
 

@@ -16,6 +16,7 @@ cudaError_t launch_chunk_plan(int R, const int32_t *ctx_len, const int32_t *n_ne
 struct RopeParams {
     unsigned long long turn[64];   // pair i: turns per position, 0.64 fixed point
     uint8_t axis[64];              // pair i: row of positions
+    float4 table[64];              // (cos, sin) of i / 64 turns as hi + lo: cos hi, sin hi, cos lo, sin lo
 };
 struct ChunkAppendParams {
     KvPool kv;                     // base, page_bytes, n_pages, types, n_layers, n_kv (no table)
@@ -26,8 +27,9 @@ struct ChunkAppendParams {
     const int64_t *slots;
     void *q_out;
     uint32_t *status;
-    int splits;                    // CTAs along y that share a token tile's query and key heads
+    int splits;                    // CTAs that share a token tile's query and key heads
     int tok_warp;                  // tokens of one warp of those
+    int qk_ctas;                   // CTAs of queries and keys; the others move values
     RopeParams rope;
 };
 cudaError_t launch_chunk_append(ChunkAppendParams p, cudaStream_t stream);

@@ -1,5 +1,7 @@
 // chunk_api.cu -- C entries of the chunk operators: argument checks and
 // launches (include/zdec.h, "chunks of new tokens").
+#include <algorithm>
+#include <array>
 #include <cmath>
 
 #include "chunk.cuh"
@@ -104,6 +106,15 @@ extern "C" zdec_status zdec_chunk_append(const zdec_pool *pool, int layer, const
     p.slots = slots_dev;
     p.q_out = q_out_dev;
     p.status = status_dev;
+    static const std::array<float4, 64> table = [] {
+        std::array<float4, 64> t;
+        for (int i = 0; i < 64; i++) {
+            const double c = std::cos(2.0 * M_PI * i / 64), s = std::sin(2.0 * M_PI * i / 64);
+            t[i] = make_float4((float)c, (float)s, (float)(c - (float)c), (float)(s - (float)s));
+        }
+        return t;
+    }();
+    std::copy(table.begin(), table.end(), p.rope.table);
     int a = 0, left = rope->sections[0];
     for (int i = 0; i < 64; i++) {
         while (left == 0) left = rope->sections[++a];
