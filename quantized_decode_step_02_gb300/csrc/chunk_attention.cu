@@ -56,6 +56,7 @@ struct CaLayout {
 constexpr uint32_t CA_WAIT_LIMIT = 1u << 31;       // clock cycles (~1 s)
 constexpr float CA_LAG = 8.0f;                     // log2 units that m may lag behind the maximum
 constexpr int PART_LD = HD + 4;                    // floats of a partial row: m, l, -, -, o[128]
+constexpr int CA_COMBINE_Y = 8;
 constexpr int CA_SEGS = 4, CA_SEG_READERS = 14;   // segments on their way; warps that read each
 
 // Workspace: one descriptor per CTA, then two partial items per CTA (0: the
@@ -87,6 +88,7 @@ struct Segment {
 struct Walk {
     ChunkReq q;
     int r, h, j, J;
+    int ov;                   // units of an item's fixed cost
     int off;                  // units of the item before this CTA's
     long long left;           // units left to this CTA
 };
@@ -116,8 +118,9 @@ __device__ __forceinline__ bool next_segment(const ChunkAttnParams &p, Walk &w, 
         }
         w.j = 0;
     }
-    const int chunks = w.q.chunks(w.j), weight = max(1, chunks);
+    const int chunks = w.q.chunks(w.j), weight = max(1, chunks) + w.ov;
     const int take = (int)min((long long)(weight - w.off), w.left);
+    const int a = max(0, w.off - w.ov), b = max(0, w.off + take - w.ov);   // of its chunks (or of the one unit of an item without)
     s.h = w.h;
     s.r = w.r;
     s.row0 = w.j * w.q.TP * p.G;
@@ -125,9 +128,9 @@ __device__ __forceinline__ bool next_segment(const ChunkAttnParams &p, Walk &w, 
     s.t0 = w.q.t0;
     s.a = w.q.a;
     s.kv = w.q.kv;
-    s.c0 = w.q.c_lo(w.j) + w.off;
-    s.n_c = chunks > 0 ? take : 0;
-    s.begins = w.off == 0;
+    s.c0 = w.q.c_lo(w.j) + a;
+    s.n_c = chunks > 0 ? b - a : 0;
+    s.begins = a == 0;
     s.ends = w.off + take == weight;
     w.left -= take;
     w.off += take;
@@ -137,7 +140,7 @@ __device__ __forceinline__ bool next_segment(const ChunkAttnParams &p, Walk &w, 
         w.off = 0;
         w.j++;
     }
-    return true;
+    return b > a;   // false: only the item's fixed cost lies in this CTA's range, which ends there
 }
 
 // Keys [lo, hi) that some row, and [all_lo, all_hi) that every row of the item sees.
@@ -180,7 +183,7 @@ struct CaShared {
     ChunkReq w_q;             // the request that holds this CTA's first unit, its index, its weight per kv head,
     int w_r;                  // and which of its units that is
     long long w_per, w_x;
-    long long scan[CA_THREADS / 32];
+    long long scan[2][CA_THREADS / 32];
     uint32_t tmem;
     int abort;
     int pages_ok[8];          // chunk i (mod 8): bit k, page k of it is in the pool
@@ -488,53 +491,71 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
     }
     mbar_fence_init();
     tc_fence_before();
+    long long items = 0, run_items = 0;   // an item costs ov units beside its chunks
+    int ov = 0;
 #pragma unroll 1
     for (int r0 = 0;;) {
-        long long my_per = 0, my_w = 0;
+        long long my_per = 0, my_w = 0, my_i = 0;
         if (r0 + tid < p.R) {
             my_q = load_req(p, r0 + tid);
             my_per = my_q.before(my_q.blocks());
             my_w = my_per * n_kv;
+            my_i = (long long)my_q.blocks() * n_kv;
         }
-        long long incl = my_w;
+        long long incl = my_w, incl_i = my_i;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(CAF, incl, o);
-            if (lane >= o) incl += v;
+            const long long v = __shfl_up_sync(CAF, incl, o), vi = __shfl_up_sync(CAF, incl_i, o);
+            if (lane >= o) {
+                incl += v;
+                incl_i += vi;
+            }
         }
-        if (lane == 31) sh.scan[warp] = incl;
+        if (lane == 31) {
+            sh.scan[0][warp] = incl;
+            sh.scan[1][warp] = incl_i;
+        }
         __syncthreads();
-        const long long base = run;
+        incl += run;
+        incl_i += run_items;
 #pragma unroll 1
         for (int i = 0; i < CA_THREADS / 32; i++) {
-            const long long v = sh.scan[i];
-            if (i < warp) incl += v;
+            const long long v = sh.scan[0][i], vi = sh.scan[1][i];
+            if (i < warp) {
+                incl += v;
+                incl_i += vi;
+            }
             run += v;
+            run_items += vi;
         }
         __syncthreads();
         if (W < 0) {                               // first time: up to all requests' weight
             r0 += CA_THREADS;
             if (r0 < p.R) continue;
-            W = run;
-            P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has work: pieces follow each other
+            // With more than two chunks per CTA an item's start and end (its Q, its O, an empty pipeline) are worth
+            // about three chunks; with fewer every chunk gets a CTA of its own.
+            ov = run > 2LL * gridDim.x ? 3 : 0;
+            items = run_items;
+            W = run + ov * items;
+            P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has units: pieces follow each other
             if (cta >= P) break;
             u0 = div_any(W * cta, P);
             u1 = div_any(W * (cta + 1), P);
+            r0 = 0;
             if (p.R > CA_THREADS) {                // second time: up to this CTA's first unit
-                r0 = 0;
                 run = 0;
+                run_items = 0;
                 continue;
             }
-            r0 = 0;
         }
-        const long long excl = base + incl - my_w;
-        if (my_w > 0 && excl <= u0 && u0 < excl + my_w) {
+        const long long mine = my_w + ov * my_i, excl = incl + ov * incl_i - mine;
+        if (mine > 0 && excl <= u0 && u0 < excl + mine) {
             sh.w_q = my_q;
             sh.w_r = r0 + tid;
-            sh.w_per = my_per;
+            sh.w_per = my_per + (long long)ov * my_q.blocks();
             sh.w_x = u0 - excl;
         }
-        if (run > u0) break;
+        if (run + ov * run_items > u0) break;
         r0 += CA_THREADS;
     }
     tc_fence_after();
@@ -734,13 +755,14 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             int a = 0, b = w.J;   // the block that holds unit y: 32 lanes try as many places at once
             while (b - a > 1) {
                 const int step = (b - a + 31) / 32, at = a + lane * step;
-                const unsigned le = __ballot_sync(CAF, at < b && w.q.before(at) <= y);
+                const unsigned le = __ballot_sync(CAF, at < b && w.q.before(at) + (long long)ov * at <= y);
                 const int k = 31 - __clz(le);   // lane 0 always holds
                 a += k * step;
                 b = min(b, a + step);
             }
             w.j = a;
-            w.off = (int)(y - (a > 0 ? w.q.before(a) : 0));
+            w.off = (int)(y - (a > 0 ? w.q.before(a) + (long long)ov * a : 0));
+            w.ov = ov;
             w.left = u1 - u0;
         }
         if (lane == 0) {
@@ -765,6 +787,8 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             const Segment s = sh.seg[si % CA_SEGS];
             const bool two = ROWS > 128 && s.rows > 128;
             const Seen seen = seen_by(p, s);
+            // chunks in [c_a, c_b) are seen whole by every row
+            const int c_a = (int)((seen.all_lo + CA_KEYS - 1) / CA_KEYS) - s.c0, c_b = (int)(seen.all_hi / CA_KEYS) - s.c0;
             for (int i = 0; ok && i < 2 * s.n_c; i++, it++) {
                 int kv, c;
                 item_at(i, s.n_c, two, kv, c);
@@ -775,32 +799,38 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                     if (!ok) break;
                     dir++;
                 } else {
-                    ok = it < NS || wait.warp(&sh.empty[sl], (it / NS - 1) & 1);
-#pragma unroll 1
-                    for (int k = 0; ok && k < 2; k++) {
-                        const uint32_t rs = raw % NR;
-                        ok = wait.warp(&sh.raw_full[rs], (raw / NR) & 1);
-                        if (!ok) break;
-                        const uint8_t *src = raws + rs * CA_RAW;
-                        if (kv) {
-                            if (p.kv.v_type == KV_T_Q8) prepare_v<true>(src, slot, th, k);
-                            else prepare_v<false>(src, slot, th, k);
-                        } else {
-                            if (p.kv.k_type == KV_T_Q8) prepare_k<true>(src, slot, th, k);
-                            else prepare_k<false>(src, slot, th, k);
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive1(&sh.raw_empty[rs]);
-                        raw++;
-                    }
+                    // three waits at once: the slot (lane 0), the raw pages (lanes 1, 2)
+                    const uint32_t mine = raw + (lane == 2), rs = mine % NR;
+                    bool there = true;
+                    if (lane == 0) there = it < NS || wait(&sh.empty[sl], (it / NS - 1) & 1);
+                    else if (lane < 3) there = wait(&sh.raw_full[rs], (mine / NR) & 1);
+                    ok = __all_sync(CAF, there);
+                    __syncwarp();
                     if (!ok) break;
+#pragma unroll 1
+                    for (int k = 0; k < 2; k++) {
+                        const uint8_t *r = raws + ((raw + k) % NR) * CA_RAW;
+                        if (kv) {
+                            if (p.kv.v_type == KV_T_Q8) prepare_v<true>(r, slot, th, k);
+                            else prepare_v<false>(r, slot, th, k);
+                        } else {
+                            if (p.kv.k_type == KV_T_Q8) prepare_k<true>(r, slot, th, k);
+                            else prepare_k<false>(r, slot, th, k);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 1 || lane == 2) mbar_arrive1(&sh.raw_empty[rs]);
+                    raw += 2;
                 }
                 if (kv) {
-                    const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
-                    const int lo = (int)max(0LL, seen.lo - key0), hi = (int)min((long long)CA_KEYS, seen.hi - key0);
                     const int pok = sh.pages_ok[(ci + c) & 7];
-                    if (lo > 0 || hi < CA_KEYS || pok != 3) clean_v(slot, th, lo, hi, pok);
-                    const bool bad = __any_sync(CAF, partly_seen(seen, key0) && v_not_finite(slot, th));
+                    bool bad = false;
+                    if (c < c_a || c >= c_b || pok != 3) {
+                        const long long key0 = (long long)(s.c0 + c) * CA_KEYS;
+                        const int lo = (int)max(0LL, seen.lo - key0), hi = (int)min((long long)CA_KEYS, seen.hi - key0);
+                        clean_v(slot, th, lo, hi, pok);
+                        bad = __any_sync(CAF, partly_seen(seen, key0) && v_not_finite(slot, th));
+                    }
                     if (lane == 0) reinterpret_cast<uint8_t *>(&sh.bad[(ci + c) & 7])[warp & 3] = bad;
                 }
                 async_proxy_fence();
@@ -1082,40 +1112,33 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
 }
 
 // Joins the pieces of the item that CTA blockIdx.x began and a later one
-// ended, in key order: one warp per row, four dims per lane.
-__global__ __launch_bounds__(1024) void chunk_combine_kernel(const __grid_constant__ ChunkAttnParams p) {
+// ended, in key order: a row per half warp, eight dims per lane, one pass with
+// the running maximum.
+__global__ __launch_bounds__(256) void chunk_combine_kernel(const __grid_constant__ ChunkAttnParams p) {
     pdl_wait();
     const CaDesc *d = reinterpret_cast<const CaDesc *>(p.ws) + blockIdx.x;
     if (!d->valid) return;
-    const int lane = threadIdx.x & 31, first = blockIdx.x, last = d->last, rows = d->rows;
-    for (int row = threadIdx.x >> 5; row < rows; row += 32) {
-        float m = -INFINITY;
-#pragma unroll 1
-        for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, *part_row(p.ws, c, c == first ? 1 : 0, row));
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(CAF, m, o));
-        float l = 0.0f;
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+    const int lane = threadIdx.x & 15, first = blockIdx.x, last = d->last, rows = d->rows;
+    for (int row = blockIdx.y * 16 + (threadIdx.x >> 4); row < rows; row += CA_COMBINE_Y * 16) {
+        float m = -INFINITY, l = 0.0f, y[8] = {};
+#pragma unroll 4
         for (int c = first; c <= last; c++) {
             const float *r = part_row(p.ws, c, c == first ? 1 : 0, row);
             const float2 ml = *reinterpret_cast<const float2 *>(r);
-            const float4 x = *reinterpret_cast<const float4 *>(r + 4 + 4 * lane);
-            const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m);
-            l += f * ml.y;
-            y.x += f * x.x; y.y += f * x.y; y.z += f * x.z; y.w += f * x.w;
+            const float4 a = *reinterpret_cast<const float4 *>(r + 4 + 8 * lane), b = *reinterpret_cast<const float4 *>(r + 8 + 8 * lane);
+            const float top = fmaxf(m, ml.x);
+            const float f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
+            m = top;
+            l = f0 * l + f1 * ml.y;
+            y[0] = f0 * y[0] + f1 * a.x; y[1] = f0 * y[1] + f1 * a.y; y[2] = f0 * y[2] + f1 * a.z; y[3] = f0 * y[3] + f1 * a.w;
+            y[4] = f0 * y[4] + f1 * b.x; y[5] = f0 * y[5] + f1 * b.y; y[6] = f0 * y[6] + f1 * b.z; y[7] = f0 * y[7] + f1 * b.w;
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int flat = d->row0 + row, tok = flat / p.G, head = d->h * p.G + flat % p.G;
-        uint16_t *out = p.o + (long long)(d->t0 + tok) * p.o_ld + (long long)head * HD + 4 * lane;
-        uint2 o2;
-        if (p.io_type == ZDEC_F16) {
-            o2.x = h2_as_u32(__floats2half2_rn(y.x * inv, y.y * inv));
-            o2.y = h2_as_u32(__floats2half2_rn(y.z * inv, y.w * inv));
-        } else {
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o2.x) : "f"(y.y * inv), "f"(y.x * inv));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o2.y) : "f"(y.w * inv), "f"(y.z * inv));
-        }
-        *reinterpret_cast<uint2 *>(out) = o2;
+        const int flat = d->row0 + row, tok = flat / p.G, head = d->h * p.G + flat - tok * p.G;
+        uint16_t *out = p.o + (long long)(d->t0 + tok) * p.o_ld + (long long)head * HD + 8 * lane;
+        *reinterpret_cast<uint4 *>(out) =
+            make_uint4(pack_out(y[0] * inv, y[1] * inv, p.io_type), pack_out(y[2] * inv, y[3] * inv, p.io_type),
+                       pack_out(y[4] * inv, y[5] * inv, p.io_type), pack_out(y[6] * inv, y[7] * inv, p.io_type));
     }
 }
 
@@ -1183,7 +1206,7 @@ cudaError_t launch_chunk_attention(const ChunkAttnParams &p0, cudaStream_t strea
     if (p.rows > 128) e = f16 ? run<256, true>(p, map, ctas, stream) : run<256, false>(p, map, ctas, stream);
     else e = f16 ? run<128, true>(p, map, ctas, stream) : run<128, false>(p, map, ctas, stream);
     if (e != cudaSuccess) return e;
-    return launch_k(chunk_combine_kernel, dim3(ctas), dim3(1024), 0, true, 1, stream, p);
+    return launch_k(chunk_combine_kernel, dim3(ctas, CA_COMBINE_Y), dim3(256), 0, true, 1, stream, p);
 }
 
 }  // namespace zdec
