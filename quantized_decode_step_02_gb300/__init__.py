@@ -527,7 +527,7 @@ class KVPool:
             raise ZdecError(-1, "bad cache type or pool shape")
         _tensor(pages, "pages", ("uint8",), (None, nbytes), None)
         self.pages, self.n_layers, self.n_kv_heads, self.k_type, self.v_type = pages, n_layers, n_kv_heads, kt, vt
-        self.device = pages.device
+        self.device, self.index = pages.device, pages.get_device()
         self._c = _Pool(pages.data_ptr(), pages.shape[0], n_layers, n_kv_heads, kt, vt)
         self._ref = ctypes.byref(self._c)
 
@@ -558,9 +558,15 @@ _DT = {}   # torch dtypes by name, and torch dtype -> zdec_float_type
 def _dtypes():
     if not _DT:
         import torch
+        if not torch.cuda.is_available():
+            raise ZdecError(-1, "the chunk operators need CUDA tensors")
         _DT.update({n: getattr(torch, n) for n in ("int32", "int64", "uint8", "float16", "bfloat16", "float32")})
         _DT.update({getattr(torch, n): t for n, t in _TYPE_ID.items()})
         _DT["torch"] = torch
+        torch.cuda.init()
+        # the current stream's handle and the current device without a Stream object in between (1 us less per call)
+        _DT["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _DT["device"] = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     return _DT
 
 
@@ -568,8 +574,7 @@ def _rows(x) -> int:
     """Elements from row to row if the rows of x are contiguous within, else 0
     (a single row's own length: its stride says nothing)."""
     if x.is_contiguous():
-        n = x.shape[1]
-        return n * x.shape[2] if x.dim() == 3 else n
+        return x.stride(0) if x.shape[0] > 1 else x[:1].numel()
     if x.dim() == 3:
         ok = x.stride(2) == 1 and x.stride(1) == x.shape[2]
         return (x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]) if ok else 0
@@ -578,13 +583,13 @@ def _rows(x) -> int:
 
 def _call(index, stream, fn, *args):
     """One stateless call on CUDA device `index`, on `stream` (a cudaStream_t, or None: torch's current stream there)."""
-    torch = _dtypes()["torch"]
+    dt = _DT
     if stream is None:
-        stream = torch.cuda.current_stream(index).cuda_stream
-    if torch.cuda.current_device() == index:
+        stream = dt["stream"](index)
+    if dt["device"]() == index:
         s = fn(*args, stream)
     else:
-        with torch.cuda.device(index):
+        with dt["torch"].cuda.device(index):
             s = fn(*args, stream)
     if s:
         _glob_check(s)
@@ -603,16 +608,22 @@ def chunk_plan(ctx_len, n_new, tables, cu, kv_len, positions, slots, taken, free
     n_new [R], tables [R, max_pages] (entries of new pages are set when
     free_pages is given), outputs cu [R + 1], kv_len [R], positions [T], taken
     [2] and int64 slots [T].  Asynchronous."""
-    dt = _dtypes()
-    i32 = dt["int32"]
-    ints = (ctx_len, n_new, tables, cu, kv_len, positions, taken)
-    quick = False
-    if all(getattr(x, "dtype", None) is i32 for x in ints) and getattr(slots, "dtype", None) is dt["int64"]:
-        R, T, idx = ctx_len.numel(), positions.numel(), ctx_len.get_device()
-        quick = (idx >= 0 and all(x.get_device() == idx and x.is_contiguous() for x in ints) and slots.get_device() == idx
-                 and slots.is_contiguous() and ctx_len.dim() == 1 and n_new.shape == (R,) and kv_len.shape == (R,)
-                 and cu.shape == (R + 1,) and tables.dim() == 2 and tables.shape[0] == R and positions.dim() == 1
-                 and slots.shape == (T,) and taken.shape == (2,))
+    dt = _DT or _dtypes()
+    i32, free, n_free = dt["int32"], None, 0
+    try:
+        R, T, idx, f = ctx_len.numel(), positions.numel(), ctx_len.get_device(), free_pages
+        quick = (idx >= 0 and ctx_len.dtype is i32 and n_new.dtype is i32 and tables.dtype is i32 and cu.dtype is i32
+                 and kv_len.dtype is i32 and positions.dtype is i32 and taken.dtype is i32 and slots.dtype is dt["int64"]
+                 and n_new.get_device() == idx and tables.get_device() == idx and cu.get_device() == idx
+                 and kv_len.get_device() == idx and positions.get_device() == idx and taken.get_device() == idx
+                 and slots.get_device() == idx and ctx_len.shape == (R,) and n_new.shape == (R,) and kv_len.shape == (R,)
+                 and cu.shape == (R + 1,) and tables.dim() == 2 and tables.shape[0] == R and positions.shape == (T,)
+                 and slots.shape == (T,) and taken.shape == (2,) and ctx_len.is_contiguous() and n_new.is_contiguous()
+                 and tables.is_contiguous() and cu.is_contiguous() and kv_len.is_contiguous() and positions.is_contiguous()
+                 and slots.is_contiguous() and taken.is_contiguous()
+                 and (f is None or (f.dtype is i32 and f.get_device() == idx and f.dim() == 1 and f.is_contiguous())))
+    except AttributeError:
+        quick = False
     if not quick:
         _tensor(ctx_len, "ctx_len", _I32, (None,), None)
         dev, R = ctx_len.device, ctx_len.shape[0]
@@ -622,9 +633,9 @@ def chunk_plan(ctx_len, n_new, tables, cu, kv_len, positions, slots, taken, free
                                (taken, "taken", (2,))):
             _tensor(x, name, _I32, shape, dev)
         _tensor(slots, "slots", _I64, (T,), dev)
-    free, n_free = None, 0
+        if free_pages is not None:
+            _tensor(free_pages, "free_pages", _I32, (None,), dev)
     if free_pages is not None:
-        _tensor(free_pages, "free_pages", _I32, (None,), ctx_len.device)
         n_free = free_pages.numel()
         free = free_pages.data_ptr() if n_free else taken.data_ptr()   # an empty list: never read, but not "no list"
     _call(idx, stream, load_library().zdec_chunk_plan, R, ctx_len.data_ptr(), n_new.data_ptr(), free, n_free, tables.data_ptr(),
@@ -647,9 +658,9 @@ def chunk_append(cache: KVPool, layer: int, qkv, positions, slots, q_out=None, r
     q_out [T, n_q, 128] fp16 or bf16 (or None: qkv holds no queries); sections:
     rotary pairs per position axis (sum 64); rope_theta 0: no rotation;
     status: optional int32 [1].  Asynchronous."""
-    dt, dev, nkv, axes = _dtypes(), cache.device, cache.n_kv_heads, len(sections)
+    dt, dev, nkv, axes = _DT or _dtypes(), cache.device, cache.n_kv_heads, len(sections)
     rope = _rope(float(rope_theta), tuple(sections))
-    idx = dev.index
+    idx = cache.index
     quick = False
     if getattr(qkv, "dtype", None) in dt and qkv.dim() == 2 and qkv.get_device() == idx:
         T, width = qkv.shape
@@ -679,10 +690,11 @@ def chunk_append(cache: KVPool, layer: int, qkv, positions, slots, q_out=None, r
 def chunk_read(cache: KVPool, layer: int, slots, k, v, status=None, stream=None):
     """K and V of the given slots [T] int64 as fp16 rows k, v [T, n_kv, 128]
     (zdec_chunk_read); negative slots read as 0.  Asynchronous."""
-    dt, dev = _dtypes(), cache.device
-    idx, want = dev.index, (getattr(slots, "shape", (0,))[0], cache.n_kv_heads, 128)
+    dt, dev = _DT or _dtypes(), cache.device
+    idx, want = cache.index, (getattr(slots, "shape", (0,))[0], cache.n_kv_heads, 128)
     if not (getattr(slots, "dtype", None) is dt["int64"] and slots.dim() == 1 and slots.get_device() == idx and slots.is_contiguous()
-            and all(x.dtype is dt["float16"] and x.shape == want and x.get_device() == idx and x.is_contiguous() for x in (k, v))):
+            and k.dtype is dt["float16"] and v.dtype is dt["float16"] and k.shape == want and v.shape == want
+            and k.get_device() == idx and v.get_device() == idx and k.is_contiguous() and v.is_contiguous()):
         _tensor(slots, "slots", _I64, (None,), dev)
         _tensor(k, "k", _HALF[:1], want, dev)
         _tensor(v, "v", _HALF[:1], want, dev)
@@ -701,14 +713,16 @@ def chunk_attention(cache: KVPool, layer: int, q, o, cu, kv_len, tables, workspa
     strided), int32 cu [R + 1], kv_len [R], tables [R, max_pages]; workspace:
     uint8 CUDA tensor of chunk_attention_workspace_bytes(n_q, n_kv) bytes, one
     per stream of calls; scale: 1 / sqrt(128) if None.  Asynchronous."""
-    dt, dev = _dtypes(), cache.device
-    idx, i32 = dev.index, dt["int32"]
+    dt, dev = _DT or _dtypes(), cache.device
+    idx, i32 = cache.index, dt["int32"]
     quick = False
     if (getattr(q, "dtype", None) is dt["float16"] or getattr(q, "dtype", None) is dt["bfloat16"]) and q.dim() == 3 and o.dim() == 3:
         R, q_ld, o_ld = kv_len.numel(), _rows(q), _rows(o)
         quick = (q.get_device() == idx and o.get_device() == idx and o.dtype is q.dtype and o.shape == q.shape and q.shape[2] == 128
                  and q_ld > 0 and o_ld > 0
-                 and all(x.dtype is i32 and x.get_device() == idx and x.is_contiguous() for x in (cu, kv_len, tables))
+                 and cu.dtype is i32 and kv_len.dtype is i32 and tables.dtype is i32 and cu.get_device() == idx
+                 and kv_len.get_device() == idx and tables.get_device() == idx and cu.is_contiguous() and kv_len.is_contiguous()
+                 and tables.is_contiguous()
                  and kv_len.dim() == 1 and cu.shape == (R + 1,) and tables.dim() == 2 and tables.shape[0] == R
                  and workspace.dtype is dt["uint8"] and workspace.get_device() == idx and workspace.is_contiguous())
     if not quick:

@@ -30,6 +30,7 @@ struct ChunkAppendParams {
     int splits;                    // CTAs that share a token tile's query and key heads
     int tok_warp;                  // tokens of one warp of those
     int qk_ctas;                   // CTAs of queries and keys; the others move values
+    int v_tile;                    // tokens of one of those
     RopeParams rope;
 };
 cudaError_t launch_chunk_append(ChunkAppendParams p, cudaStream_t stream);

@@ -115,15 +115,23 @@ extern "C" zdec_status zdec_chunk_append(const zdec_pool *pool, int layer, const
         return t;
     }();
     std::copy(table.begin(), table.end(), p.rope.table);
+    // the fraction of a turn per position, as 0.64 fixed point: whole turns drop out (computed anew when theta changes)
+    thread_local float known = -1.0f;
+    thread_local unsigned long long turn[64];
+    if (known != rope->theta) {
+        for (int i = 0; i < 64; i++) {
+            double t = rope->theta > 0.0f ? std::pow((double)rope->theta, -i / 64.0) / (2.0 * M_PI) : 0.0;
+            t -= std::floor(t);
+            turn[i] = (unsigned long long)std::ldexp(t, 64);
+        }
+        known = rope->theta;
+    }
+    std::copy(turn, turn + 64, p.rope.turn);
     int a = 0, left = rope->sections[0];
     for (int i = 0; i < 64; i++) {
         while (left == 0) left = rope->sections[++a];
         left--;
         p.rope.axis[i] = (uint8_t)a;
-        // the fraction of a turn per position, as 0.64 fixed point: whole turns drop out
-        double t = rope->theta > 0.0f ? std::pow((double)rope->theta, -i / 64.0) / (2.0 * M_PI) : 0.0;
-        t -= std::floor(t);
-        p.rope.turn[i] = (unsigned long long)std::ldexp(t, 64);
     }
     CK(launch_chunk_append(p, (cudaStream_t)stream));
     return ZDEC_OK;

@@ -365,57 +365,61 @@ __device__ __forceinline__ float v_at(const uint8_t *slot, int j, int d) {
 }
 
 // The 32 rows of a warp into its part of a Q operand tile, two rows of 16
-// lanes x 16 bytes at a time (`src`: this lane's row).  fp16 as it is; a bf16
-// row times 2^-e, which brings its largest element below fp16's top (exact but
-// for elements below 2^-28 of it).  Returns e of this lane's row.
-__device__ __forceinline__ int load_q(const uint16_t *src, int io_type, bool store, uint8_t *tile, int row0) {
+// lanes x 16 bytes at a time (`src`: this lane's row), all loads in flight
+// together.  fp16 as it is; a bf16 row times 2^-e, which brings its largest
+// element below fp16's top (exact but for elements below 2^-28 of it): in
+// place afterwards.  Returns e of this lane's row.  Rows from n_rows on stay as
+// they are: a row of the MMA touches no other.
+__device__ __forceinline__ int load_q(const uint16_t *src, int io_type, bool store, uint8_t *tile, int row0, int n_rows) {
     const int lane = threadIdx.x & 31, c = lane & 15, up = lane >> 4;
+    uint8_t *to = tile + (c >> 3) * 16384 + (row0 + up) * 128;
+    if (store) {
+#pragma unroll 1
+        for (int i0 = 0; 2 * i0 < n_rows; i0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * (i0 + i) + up);
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(from) + c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                *reinterpret_cast<uint4 *>(to + (i0 + i) * 256 + (((c ^ (2 * (i0 + i) + up)) & 7) << 4)) = v[i];
+        }
+    }
+    if (io_type == ZDEC_F16) return 0;
     int mine = 0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint4 v[8];
+    for (int i = 0; 2 * i < n_rows; i++) {
+        uint4 *at = reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4));
+        const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * i + up);
+        const uint4 x = store ? *at : __ldg(reinterpret_cast<const uint4 *>(from) + c);
+        uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;   // largest magnitude bits of the row
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * (i0 + i) + up);
-            v[i] = __ldg(reinterpret_cast<const uint4 *>(from) + c);
-        }
-        uint8_t *to = tile + (c >> 3) * 16384 + (row0 + 2 * i0 + up) * 128;
-        if (io_type == ZDEC_F16) {
+        for (int k = 0; k < 4; k++) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (store) *reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4)) = v[i];
-            continue;
-        }
-#pragma unroll 1
-        for (int i = 0; i < 8; i++) {
-            uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, top = 0;   // largest magnitude bits of the row
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(CAF, top, o));
+        const int ex = (int)(top >> 7);                  // biased exponent
+        const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
+        const int both = __shfl_sync(CAF, e, (lane & 1) * 16);
+        if ((lane >> 1) == i) mine = both;
+        // 2^-e, e in [-140, 113]: 2^140 in two steps
+        const float f1 = __int_as_float((127 + min(-e, 100)) << 23), f2 = __int_as_float((127 + max(-e - 100, 0)) << 23);
 #pragma unroll
-            for (int k = 0; k < 7; k++) v[k] = v[k + 1];
-#pragma unroll
-            for (int k = 0; k < 4; k++) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(CAF, top, o));
-            const int ex = (int)(top >> 7);                  // biased exponent
-            const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
-            const int both = __shfl_sync(CAF, e, (lane & 1) * 16);
-            if ((lane >> 1) == i0 + i) mine = both;
-            // 2^-e, e in [-140, 113]: 2^140 in two steps
-            const float f1 = __int_as_float((127 + min(-e, 100)) << 23), f2 = __int_as_float((127 + max(-e - 100, 0)) << 23);
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                w[k] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2));
-            if (store) *reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int k = 0; k < 4; k++)
+            w[k] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2));
+        if (store) *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return mine;
 }
 // 256 bytes of each of a warp's 32 rows, staged in shared memory in the same
 // arrangement, to `dst` (this lane's row; null: not written).
-__device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, uint8_t *dst) {
+__device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, int n_rows, uint8_t *dst) {
     const int lane = threadIdx.x & 31, c = lane & 15;
     __syncwarp();
 #pragma unroll 4
     for (int i = 0; i < 16; i++) {
+        if (2 * i >= n_rows) break;
         const int row = row0 + 2 * i + (lane >> 4);
         uint8_t *to = (uint8_t *)__shfl_sync(CAF, (unsigned long long)dst, 2 * i + (lane >> 4));
         const uint4 x = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
@@ -485,12 +489,11 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
     int P = 0;
     if (warp == 1) tmem_alloc(&sh.tmem, 512);
     for (int i = tid; i < CA_BARS; i += CA_THREADS) mbar_init(&sh.bars[i], bar_count(i));
-    if (tid == 0) {
-        desc->valid = 0;
-        sh.abort = 0;
-    }
+    if (tid == 0) sh.abort = 0;
     mbar_fence_init();
     tc_fence_before();
+    if (ROWS == 128) pdl_wait();   // short items: started while the kernel before ends; it wrote the inputs, or reads the workspace
+    if (tid == 0) desc->valid = 0;
     long long items = 0, run_items = 0;   // an item costs ov units beside its chunks
     int ov = 0;
 #pragma unroll 1
@@ -533,8 +536,8 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             r0 += CA_THREADS;
             if (r0 < p.R) continue;
             // With more than two chunks per CTA an item's start and end (its Q, its O, an empty pipeline) are worth
-            // about three chunks; with fewer every chunk gets a CTA of its own.
-            ov = run > 2LL * gridDim.x ? 3 : 0;
+            // about three chunks of 256 rows or four of 128; with fewer every chunk gets a CTA of its own.
+            ov = run > 2LL * gridDim.x ? (ROWS > 128 ? 3 : 4) : 0;
             items = run_items;
             W = run + ov * items;
             P = (int)min((long long)gridDim.x, W);   // every CTA of the first P has units: pieces follow each other
@@ -581,9 +584,9 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
         si++;
     };
 
-    // registers: 4 warpgroups x 128 at launch = 64 + 80 (or 56 + 88) + 2 x 184
+    // registers: 4 warpgroups x 128 at launch = 64 + 80 + 2 x 184, or 64 + 96 + 2 x 176; short items need no other split
     if (group == 0) {
-    reg_dec<ALL_F16 ? 64 : 56>();
+    if (ROWS > 128) reg_dec<64>();
     if (warp == 0) {
         // ---------------------------------------------------------- copies ---
         const uint32_t kb = kv_region_bytes(p.kv.k_type), vb = kv_region_bytes(p.kv.v_type);
@@ -779,7 +782,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
     }
     } else if (group == 3) {
         // ------------------------------------------------------- preparing ---
-        reg_dec<ALL_F16 ? 80 : 88>();
+        if (ROWS > 128) reg_dec<ALL_F16 ? 80 : 96>();
         const int th = tid - 384;
         uint32_t it = 0, dir = 0, raw = 0, ci = 0;   // operands, those landing as such, raw pages; chunks
         bool ok = true;
@@ -841,7 +844,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
         }
     } else {
         // --------------------------------------------------------- softmax ---
-        reg_inc<184>();
+        if (ROWS > 128) reg_inc<ALL_F16 ? 184 : 176>();
         const int u = group - 1, w4 = warp & 3, row = w4 * 32 + lane;     // buffer; TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)w4 << 21);           // lanes 32 (warp % 4) ..
         const uint32_t s_addr = lane_base + u * 128, o_addr = lane_base + 256 + u * 128;
@@ -870,7 +873,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             if (act) {
                 const uint16_t *src = p.q + (long long)(s.t0 + tok) * p.q_ld + (long long)head * HD;
                 const bool mine = two || u == 0;
-                const int e = mine || p.io_type != ZDEC_F16 ? load_q(src, p.io_type, mine, q_smem + first * 256, w4 * 32) : 0;
+                const int e = mine || p.io_type != ZDEC_F16 ? load_q(src, p.io_type, mine, q_smem + first * 256, w4 * 32, min(32, rows - first - w4 * 32)) : 0;
                 scale = fmaxf(ldexpf(p.scale_log2, e), 7.9e-31f);   // never 0 (0 * -inf)
             }
             if (two || u == 0) {
@@ -1085,7 +1088,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
                             for (int k = 0; k < 8; k++)
                                 stage(tile, row, 8 * (g & 1) + k, x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                         }
-                        if (whole ? g == 3 : g & 1) flush_rows(tile, w4 * 32, !dst || whole ? dst : dst + 256 * (g >> 1));
+                        if (whole ? g == 3 : g & 1) flush_rows(tile, w4 * 32, min(32, rows - first - w4 * 32), !dst || whole ? dst : dst + 256 * (g >> 1));
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1115,6 +1118,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
 // ended, in key order: a row per half warp, eight dims per lane, one pass with
 // the running maximum.
 __global__ __launch_bounds__(256) void chunk_combine_kernel(const __grid_constant__ ChunkAttnParams p) {
+    pdl_launch_dependents();
     pdl_wait();
     const CaDesc *d = reinterpret_cast<const CaDesc *>(p.ws) + blockIdx.x;
     if (!d->valid) return;
@@ -1177,7 +1181,7 @@ static cudaError_t allow_smem() {
 }
 template <int ROWS, bool ALL_F16>
 static cudaError_t run(const ChunkAttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream) {
-    return launch_k(chunk_attention_kernel<ROWS, ALL_F16>, dim3(ctas), dim3(CA_THREADS), ca_smem<ROWS, ALL_F16>, false, 1, stream, p, map);
+    return launch_k(chunk_attention_kernel<ROWS, ALL_F16>, dim3(ctas), dim3(CA_THREADS), ca_smem<ROWS, ALL_F16>, ROWS == 128, 1, stream, p, map);
 }
 
 cudaError_t launch_chunk_attention(const ChunkAttnParams &p0, cudaStream_t stream) {
