@@ -197,6 +197,30 @@ __device__ __forceinline__ uint32_t q8_code(float x, float d) {
     const int q = max(-127, min(127, __float2int_rn(__fdiv_rn(x, d))));
     return (uint32_t)(q + 128) & 0xFFu;
 }
+// Eight of them.  x times the reciprocal lies within 1e-4 of the rounded
+// quotient (127 x 7 2^-24), so where it is not within that of a half, both
+// round to the same integer, read off a sum with 1.5 2^23 + 128; else (and for
+// what is not finite) the eight are divided.
+__device__ __forceinline__ uint2 q8_codes(const float (&f)[8], float d) {
+    const float inv = d == 0.0f ? 0.0f : __fdividef(1.0f, d);
+    uint32_t c[2], t[8];
+    bool near = true;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const float r = __fmul_rn(f[k], inv), s = __fadd_rn(r, 12583040.0f);
+        near = near && fabsf(r - __fadd_rn(s, -12583040.0f)) < 0.4999f;
+        t[k] = __float_as_uint(s);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        c[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
+    if (!near) {
+        c[0] = c[1] = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; k++) c[k >> 2] |= q8_code(f[k], d) << (8 * (k & 3));
+    }
+    return make_uint2(c[0], c[1]);
+}
 // A block's scale from its amax: fp32 IEEE division (0 for an all-zero block).
 __device__ __forceinline__ float q8_scale(float amax) { return amax == 0.0f ? 0.0f : __fdiv_rn(amax, 127.0f); }
 
@@ -219,10 +243,8 @@ __device__ __forceinline__ uint4 encode8(const float (&x)[8], float &scale) {
     m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
     m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
     scale = q8_scale(m);
-    uint32_t c[2] = {0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 8; k++) c[k >> 2] |= q8_code(f[k], scale) << (8 * (k & 3));
-    return make_uint4(c[0], c[1], 0u, 0u);
+    const uint2 c = q8_codes(f, scale);
+    return make_uint4(c.x, c.y, 0u, 0u);
 }
 
 constexpr int AP_THREADS = 256, AP_WARPS = AP_THREADS / 32, AP_TILE = 64;   // AP_TILE: most tokens of a value-head CTA
@@ -314,17 +336,33 @@ __device__ __forceinline__ void append_qk(const ChunkAppendParams &p, long long 
     }
 }
 
-// What thread `i` of a tile's tokens does with the 16-byte value segments of
-// `seg` tokens: 1 the token opens a segment that the tile fills, 0 it lies
-// inside one, 2 its element goes alone, 3 it has no slot.
-__device__ __forceinline__ uint8_t segment_role(const long long *s_slot, int i, int n, int seg) {
-    const long long slot = s_slot[i];
-    if (slot < 0) return 3;
-    const int in = (int)(slot & (seg - 1)), a = i - in;   // a: where the segment's first token would be
-    if (a < 0 || a + seg > n) return 2;
-    for (int e = 0; e < seg; e++)
-        if (s_slot[a + e] != slot - in + e) return 2;
-    return in == 0;
+// What a tile's tokens do with the 16-byte value segments of `seg` tokens: 1
+// the token opens a segment that the tile fills, 0 it lies inside one, 2 its
+// element goes alone, 3 it has no slot.  Threads 0 to 63 ask, one token each;
+// `todo` gets a bit per token that is not 0.
+__device__ __forceinline__ void segment_roles(const long long *s_slot, int n, int seg, uint8_t *role, uint32_t *todo) {
+    const int i = threadIdx.x;
+    if (i >= AP_TILE) return;
+    int r = 0;
+    if (i < n) {
+        const long long slot = s_slot[i];
+        const int in = (int)(slot & (seg - 1)), a = i - in;   // a: where the segment's first token would be
+        r = slot < 0 ? 3 : a < 0 || a + seg > n ? 2 : in == 0;
+        if (r < 2) {
+            bool whole = true;
+#pragma unroll 8
+            for (int e = 0; e < seg; e++) whole = whole && s_slot[a + e] == slot - in + e;
+            if (!whole) r = 2;
+        }
+        role[i] = (uint8_t)r;
+    }
+    const uint32_t bits = __ballot_sync(FULL, r != 0);
+    if ((i & 31) == 0) todo[i >> 5] = bits;
+}
+// The bits of tokens lo .. lo + len - 1 (len <= 32), lo a multiple of len.
+__device__ __forceinline__ uint32_t todo_of(const uint32_t *todo, int lo, int len) {
+    const uint32_t w = todo[lo >> 5] >> (lo & 31);
+    return len == 32 ? w : w & ((1u << len) - 1);
 }
 
 // One value head of up to AP_TILE tokens: encoded rows meet in shared memory
@@ -332,7 +370,7 @@ __device__ __forceinline__ uint8_t segment_role(const long long *s_slot, int i, 
 // those tokens fill one 16-byte segment of the page, else element by element.
 template <int IN, int VT>
 __device__ __forceinline__ void append_v(const ChunkAppendParams &p, long long tile, int head, uint8_t *smem, long long *s_slot,
-                                         uint8_t *s_role) {
+                                         uint8_t *s_role, uint32_t *s_todo) {
     constexpr int ES = VT == KV_T_F16 ? 2 : 1, SEG = 16 / ES;
     constexpr int PITCH = HD * ES + 16;   // bytes of a row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 15;
@@ -340,7 +378,7 @@ __device__ __forceinline__ void append_v(const ChunkAppendParams &p, long long t
     const int n = (int)min((long long)p.v_tile, p.T - t0);
     if ((int)threadIdx.x < n) s_slot[threadIdx.x] = checked_slot(p.kv, __ldg(p.slots + t0 + threadIdx.x), p.status);
     __syncthreads();
-    if ((int)threadIdx.x < n) s_role[threadIdx.x] = segment_role(s_slot, threadIdx.x, n, SEG);
+    segment_roles(s_slot, n, SEG, s_role, s_todo);
     const long long col = (long long)(p.nq + p.kv.n_kv + head) * HD;
 #pragma unroll 2
     for (int i0 = 2 * warp; i0 < n; i0 += 2 * AP_WARPS) {   // two tokens of 16 lanes x 8 dims
@@ -358,10 +396,11 @@ __device__ __forceinline__ void append_v(const ChunkAppendParams &p, long long t
         }
     }
     __syncthreads();
-    const int d = threadIdx.x & (HD - 1);
-    for (int i = threadIdx.x >> 7; i < n; i += AP_THREADS / HD) {
-        const int role = s_role[i];
-        if (role == 0 || role == 3) continue;
+    // thread = dim and half of the tokens
+    const int d = threadIdx.x & (HD - 1), half = p.v_tile / 2, first = (threadIdx.x >> 7) * half;
+    for (uint32_t bits = todo_of(s_todo, first, half); bits; bits &= bits - 1) {
+        const int i = first + __ffs(bits) - 1, role = s_role[i];
+        if (role == 3) continue;
         const long long slot = s_slot[i];
         uint8_t *reg = chunk_of_page(p.kv, p.layer, head, slot >> 6) + kv_region_bytes(p.kv.k_type);
         const int tl = (int)(slot & 63);
@@ -388,7 +427,7 @@ template <int IN>
 __global__ __launch_bounds__(AP_THREADS) void chunk_append_kernel(const __grid_constant__ ChunkAppendParams p) {
     union Shared {
         struct { unsigned long long turn[64]; float4 table[64]; float2 cs[AP_WARPS][64]; uint8_t axis[64]; } qk;
-        struct { uint8_t v[AP_TILE * (HD * 2 + 16)]; long long slot[AP_TILE]; uint8_t role[AP_TILE]; } v;
+        struct { uint8_t v[AP_TILE * (HD * 2 + 16)]; long long slot[AP_TILE]; uint8_t role[AP_TILE]; uint32_t todo[2]; } v;
     };
     __shared__ __align__(16) Shared s;
     if ((int)blockIdx.x < p.qk_ctas) {
@@ -410,9 +449,9 @@ __global__ __launch_bounds__(AP_THREADS) void chunk_append_kernel(const __grid_c
         const long long tile = v / p.kv.n_kv;
         const int head = v % p.kv.n_kv;
         switch (p.kv.v_type) {
-            case KV_T_F16: append_v<IN, KV_T_F16>(p, tile, head, s.v.v, s.v.slot, s.v.role); break;
-            case KV_T_Q8: append_v<IN, KV_T_Q8>(p, tile, head, s.v.v, s.v.slot, s.v.role); break;
-            default: append_v<IN, KV_T_FP8>(p, tile, head, s.v.v, s.v.slot, s.v.role); break;
+            case KV_T_F16: append_v<IN, KV_T_F16>(p, tile, head, s.v.v, s.v.slot, s.v.role, s.v.todo); break;
+            case KV_T_Q8: append_v<IN, KV_T_Q8>(p, tile, head, s.v.v, s.v.slot, s.v.role, s.v.todo); break;
+            default: append_v<IN, KV_T_FP8>(p, tile, head, s.v.v, s.v.slot, s.v.role, s.v.todo); break;
         }
     }
 }
@@ -438,105 +477,134 @@ cudaError_t launch_chunk_append(ChunkAppendParams p, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ read ---
-// A stored Q8_0 code times its scale, exact in fp32, at most fp16's largest
-// value (127 x a scale of 516 lies past it).
-__device__ __forceinline__ float q8_value(float scale, uint32_t code) {
-    const float x = scale * (float)((int)code - 128);
-    return x > 65504.0f ? 65504.0f : (x < -65504.0f ? -65504.0f : x);
+// Two stored values (the bytes of `c` that `sel` picks, as __byte_perm does
+// with 0x64 as byte 4) as fp16: for Q8_0 1024 + code read as fp16, less 1152,
+// times the scale (the product of 8 and 11 bits, rounded once), at most fp16's
+// largest value (127 x a scale of 516 lies past it; `big`: a scale above 511).
+__device__ __forceinline__ uint32_t q8_pair(uint32_t c, uint32_t sel, uint32_t scale2, bool big) {
+    __half2 x = __hmul2(__hsub2(u32_as_h2(__byte_perm(c, 0x64u, sel)), u32_as_h2(0x64806480u)), u32_as_h2(scale2));
+    if (big) x = __hmax2_nan(__hmin2_nan(x, u32_as_h2(0x7BFF7BFFu)), u32_as_h2(0xFBFFFBFFu));
+    return h2_as_u32(x);
 }
+__device__ __forceinline__ bool big_scale(uint32_t bits) { return (bits & 0x7FFFu) > 0x5FFCu; }   // above 511, or not finite
 // Eight codes -> eight fp16.
-__device__ __forceinline__ uint4 decode8(uint2 c, int type, float scale) {
-    const uint32_t w[2] = {c.x, c.y};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        if (type == KV_T_FP8) {
-            o[2 * i] = e4m3x2_to_h2((uint16_t)w[i]);
-            o[2 * i + 1] = e4m3x2_to_h2((uint16_t)(w[i] >> 16));
-        } else {
-            o[2 * i] = pack_f16(q8_value(scale, w[i] & 255u), q8_value(scale, (w[i] >> 8) & 255u));
-            o[2 * i + 1] = pack_f16(q8_value(scale, (w[i] >> 16) & 255u), q8_value(scale, w[i] >> 24));
-        }
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+template <int T>
+__device__ __forceinline__ uint4 decode8(uint2 c, uint32_t scale) {
+    if (T == KV_T_FP8)
+        return make_uint4(e4m3x2_to_h2((uint16_t)c.x), e4m3x2_to_h2((uint16_t)(c.x >> 16)), e4m3x2_to_h2((uint16_t)c.y),
+                          e4m3x2_to_h2((uint16_t)(c.y >> 16)));
+    const uint32_t s2 = scale * 0x10001u;
+    const bool big = big_scale(scale);
+    return make_uint4(q8_pair(c.x, 0x4140, s2, big), q8_pair(c.x, 0x4342, s2, big), q8_pair(c.y, 0x4140, s2, big),
+                      q8_pair(c.y, 0x4342, s2, big));
 }
 
-// A CTA reads one kv head of up to AP_TILE slots.  K rows go straight through,
-// 16 lanes x 8 dims each; V goes through shared memory, a 16-byte segment (8
-// or 16 tokens of one dim) at a time where the tile's slots fill it.
+// A CTA reads one kv head of up to AP_TILE slots.  K rows go straight through
+// registers; V goes through shared memory, a 16-byte segment (8
+// or 16 tokens of one dim) at a time where the tile's slots fill it: a thread
+// takes two dims and a quarter of the tokens, the lane halves of a warp
+// neighbouring quarters (whole 32-byte sectors), and puts the two dims down
+// as one word, columns swapped so that the lane halves' rows, 16 apart, do not
+// meet in a bank.
+template <int KT, int VT>
 __global__ __launch_bounds__(AP_THREADS) void chunk_read_kernel(const __grid_constant__ KvPool a, int layer, int T, int tile,
                                                                 const int64_t *__restrict__ slots, uint16_t *__restrict__ k,
                                                                 uint16_t *__restrict__ v, uint32_t *status) {
-    constexpr int PITCH = HD * 2 + 16;
-    __shared__ __align__(16) uint8_t s_v[AP_TILE * PITCH];
+    constexpr int SEG = VT == KV_T_F16 ? 8 : 16;
+    __shared__ __align__(16) uint32_t s_v[AP_TILE * HD / 2];
     __shared__ long long s_slot[AP_TILE];
+    __shared__ uint32_t s_todo[2];
+    __shared__ uint32_t s_scale[AP_TILE][4];   // a block's scale, twice
     __shared__ uint8_t s_role[AP_TILE];
-    __shared__ float s_scale[AP_TILE][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 15;
     const long long t0 = (long long)(blockIdx.x / a.n_kv) * tile;
     const int head = blockIdx.x % a.n_kv, n = (int)min((long long)tile, T - t0);
-    const int seg = a.v_type == KV_T_F16 ? 8 : 16;
     if ((int)threadIdx.x < n) s_slot[threadIdx.x] = checked_slot(a, __ldg(slots + t0 + threadIdx.x), status);
     __syncthreads();
-    if ((int)threadIdx.x < n) s_role[threadIdx.x] = segment_role(s_slot, threadIdx.x, n, seg);
-    if (a.v_type == KV_T_Q8 && (int)threadIdx.x < 4 * n) {
-        const long long slot = s_slot[threadIdx.x >> 2];
-        if (slot >= 0)
-            s_scale[threadIdx.x >> 2][threadIdx.x & 3] = __half2float(*reinterpret_cast<const __half *>(
-                chunk_of_page(a, layer, head, slot >> 6) + kv_region_bytes(a.k_type) + vs_off((int)(slot & 63), threadIdx.x & 3)));
+    // K's rows on their way first: two tokens of 16 lanes x 8 dims per warp
+    uint4 kx[AP_TILE / (2 * AP_WARPS)];
+    uint32_t ks[AP_TILE / (2 * AP_WARPS)];
+#pragma unroll
+    for (int m = 0; m < AP_TILE / (2 * AP_WARPS); m++) {
+        const int i = 2 * (warp + m * AP_WARPS) + (lane >> 4);
+        const long long slot = i < n ? s_slot[i] : -1;
+        kx[m] = make_uint4(0u, 0u, 0u, 0u);
+        ks[m] = 0u;
+        if (slot < 0) {
+            if (KT == KV_T_Q8) kx[m].x = kx[m].y = 0x80808080u;
+            continue;
+        }
+        const uint8_t *reg = chunk_of_page(a, layer, head, slot >> 6);
+        const int tl = (int)(slot & 63);
+        if (KT == KV_T_F16) {
+            kx[m] = *reinterpret_cast<const uint4 *>(reg + k16_off(tl, 8 * j));
+        } else {
+            const uint2 c = *reinterpret_cast<const uint2 *>(reg + k8_off(tl, 8 * j));
+            kx[m].x = c.x;
+            kx[m].y = c.y;
+            if (KT == KV_T_Q8) ks[m] = *reinterpret_cast<const uint16_t *>(reg + ks_off(tl, j >> 2));
+        }
     }
-    __syncthreads();
-    // V: thread = dim
-    const int d = threadIdx.x & (HD - 1);
-#pragma unroll 4
-    for (int i = threadIdx.x >> 7; i < n; i += AP_THREADS / HD) {
-        const int role = s_role[i];
-        uint16_t *dst = reinterpret_cast<uint16_t *>(s_v + i * PITCH) + d;
-        if (role == 0) continue;
-        if (role == 3) { *dst = 0; continue; }
+    segment_roles(s_slot, n, SEG, s_role, s_todo);
+    bool big = false;
+    if (VT == KV_T_Q8 && (int)threadIdx.x < 4 * n) {
+        const long long slot = s_slot[threadIdx.x >> 2];
+        if (slot >= 0) {
+            const uint32_t s = *reinterpret_cast<const uint16_t *>(chunk_of_page(a, layer, head, slot >> 6) +
+                                                                   kv_region_bytes(a.k_type) +
+                                                                   vs_off((int)(slot & 63), threadIdx.x & 3));
+            s_scale[threadIdx.x >> 2][threadIdx.x & 3] = s * 0x10001u;
+            big = big_scale(s);
+        }
+    }
+    big = __syncthreads_or(big);
+    // V
+    const int dp = (lane & 15) + 16 * (warp & 3), quarter = tile / 4, first = ((lane >> 4) + 2 * (warp >> 2)) * quarter;
+    for (uint32_t bits = todo_of(s_todo, first, quarter); bits; bits &= bits - 1) {
+        const int i = first + __ffs(bits) - 1, role = s_role[i];
+        auto put = [&](int e, uint32_t w) { s_v[(i + e) * (HD / 2) + (dp ^ ((i + e) & 16))] = w; };
+        if (role == 3) { put(0, 0u); continue; }
         const long long slot = s_slot[i];
         const int tl = (int)(slot & 63);
         const uint8_t *reg = chunk_of_page(a, layer, head, slot >> 6) + kv_region_bytes(a.k_type);
-        if (a.v_type == KV_T_F16) {
-            const uint8_t *src = reg + v16_off(tl, d);
-            if (role == 2) { *dst = *reinterpret_cast<const uint16_t *>(src); continue; }
-            const uint4 x = *reinterpret_cast<const uint4 *>(src);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if (VT == KV_T_F16) {
+            const uint8_t *s0 = reg + v16_off(tl, 2 * dp), *s1 = reg + v16_off(tl, 2 * dp + 1);
+            if (role == 2) {
+                put(0, *reinterpret_cast<const uint16_t *>(s0) | ((uint32_t)*reinterpret_cast<const uint16_t *>(s1) << 16));
+                continue;
+            }
+            const uint4 x = *reinterpret_cast<const uint4 *>(s0), y = *reinterpret_cast<const uint4 *>(s1);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 8; e++) dst[e * (PITCH / 2)] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            for (int e = 0; e < 8; e++) put(e, __byte_perm(xw[e >> 1], yw[e >> 1], e & 1 ? 0x7632 : 0x5410));
         } else {
-            const uint8_t *src = reg + v8_off(tl, d);
-            const int m = role == 2 ? 1 : 16;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (role == 2) x.x = *src;
-            else x = *reinterpret_cast<const uint4 *>(src);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint8_t *s0 = reg + v8_off(tl, 2 * dp), *s1 = reg + v8_off(tl, 2 * dp + 1);
+            const uint32_t *sc = s_scale[i] + (dp >> 4);
+            if (role == 2) {
+                const uint32_t c = *s0 | ((uint32_t)*s1 << 8);
+                put(0, VT == KV_T_FP8 ? e4m3x2_to_h2((uint16_t)c) : q8_pair(c, 0x4140, *sc, big));
+                continue;
+            }
+            const uint4 x = *reinterpret_cast<const uint4 *>(s0), y = *reinterpret_cast<const uint4 *>(s1);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 16; e++) {
-                if (e >= m) break;
-                const uint32_t c = (w[e >> 2] >> (8 * (e & 3))) & 255u;
-                dst[e * (PITCH / 2)] = a.v_type == KV_T_FP8 ? (uint16_t)(e4m3x2_to_h2((uint16_t)c) & 0xFFFFu)
-                                                            : __half_as_ushort(__float2half_rn(q8_value(s_scale[i + e][d >> 5], c)));
+            for (int e = 0; e < 16; e += 2) {
+                const uint32_t c = __byte_perm(xw[e >> 2], yw[e >> 2], e & 2 ? 0x7362 : 0x5140);   // both dims of two tokens
+                if (VT == KV_T_FP8) {
+                    put(e, e4m3x2_to_h2((uint16_t)c));
+                    put(e + 1, e4m3x2_to_h2((uint16_t)(c >> 16)));
+                } else {
+                    put(e, q8_pair(c, 0x4140, sc[4 * e], big));
+                    put(e + 1, q8_pair(c, 0x4342, sc[4 * e + 4], big));
+                }
             }
         }
     }
-    // K meanwhile: two tokens per warp
-#pragma unroll 4
-    for (int i0 = 2 * warp; i0 < n; i0 += 2 * AP_WARPS) {
-        const int i = i0 + (lane >> 4);
+#pragma unroll
+    for (int m = 0; m < AP_TILE / (2 * AP_WARPS); m++) {
+        const int i = 2 * (warp + m * AP_WARPS) + (lane >> 4);
         if (i >= n) continue;
-        const long long slot = s_slot[i];
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (slot >= 0) {
-            const uint8_t *reg = chunk_of_page(a, layer, head, slot >> 6);
-            const int tl = (int)(slot & 63);
-            if (a.k_type == KV_T_F16) {
-                o = *reinterpret_cast<const uint4 *>(reg + k16_off(tl, 8 * j));
-            } else {
-                const float s = a.k_type == KV_T_Q8 ? __half2float(*reinterpret_cast<const __half *>(reg + ks_off(tl, j >> 2))) : 0.0f;
-                o = decode8(*reinterpret_cast<const uint2 *>(reg + k8_off(tl, 8 * j)), a.k_type, s);
-            }
-        }
+        const uint4 o = KT == KV_T_F16 ? kx[m] : decode8<KT>(make_uint2(kx[m].x, kx[m].y), ks[m]);
         __stcs(reinterpret_cast<uint4 *>(k + ((t0 + i) * a.n_kv + head) * HD + 8 * j), o);
     }
     __syncthreads();
@@ -545,16 +613,30 @@ __global__ __launch_bounds__(AP_THREADS) void chunk_read_kernel(const __grid_con
         const int i = i0 + (lane >> 4);
         if (i < n)
             __stcs(reinterpret_cast<uint4 *>(v + ((t0 + i) * a.n_kv + head) * HD + 8 * j),
-                   *reinterpret_cast<const uint4 *>(s_v + i * PITCH + 16 * j));
+                   *reinterpret_cast<const uint4 *>(s_v + i * (HD / 2) + ((4 * j) ^ (i & 16))));
     }
 }
 
+template <int KT>
+static void read_of_key(unsigned grid, const KvPool &kv, int layer, int T, int tile, const int64_t *slots, uint16_t *k,
+                        uint16_t *v, uint32_t *status, cudaStream_t stream) {
+    switch (kv.v_type) {
+        case KV_T_F16: chunk_read_kernel<KT, KV_T_F16><<<grid, AP_THREADS, 0, stream>>>(kv, layer, T, tile, slots, k, v, status); break;
+        case KV_T_Q8: chunk_read_kernel<KT, KV_T_Q8><<<grid, AP_THREADS, 0, stream>>>(kv, layer, T, tile, slots, k, v, status); break;
+        default: chunk_read_kernel<KT, KV_T_FP8><<<grid, AP_THREADS, 0, stream>>>(kv, layer, T, tile, slots, k, v, status); break;
+    }
+}
 cudaError_t launch_chunk_read(const KvPool &kv, int layer, int T, const int64_t *slots, uint16_t *k, uint16_t *v,
                               uint32_t *status, cudaStream_t stream) {
     const int tile = value_tile(T, kv.n_kv);
     const long long ctas = ((long long)T + tile - 1) / tile * kv.n_kv;
     if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    chunk_read_kernel<<<(unsigned)ctas, AP_THREADS, 0, stream>>>(kv, layer, T, tile, slots, k, v, status);
+    const unsigned grid = (unsigned)ctas;
+    switch (kv.k_type) {
+        case KV_T_F16: read_of_key<KV_T_F16>(grid, kv, layer, T, tile, slots, k, v, status, stream); break;
+        case KV_T_Q8: read_of_key<KV_T_Q8>(grid, kv, layer, T, tile, slots, k, v, status, stream); break;
+        default: read_of_key<KV_T_FP8>(grid, kv, layer, T, tile, slots, k, v, status, stream); break;
+    }
     return cudaGetLastError();
 }
 
