@@ -460,7 +460,7 @@ cudaError_t launch_chunk_append(ChunkAppendParams p, cudaStream_t stream) {
     const int groups = (p.nq + p.kv.n_kv + 3) / 4;
     // Few tokens: their heads are split until a wave of CTAs is full; many: a warp takes two tokens, which halves the
     // CTAs' start (tables into shared memory).
-    p.tok_warp = p.T > 2 * 152 * AP_WARPS ? 2 : 1;
+    p.tok_warp = p.T > 4 * 152 * AP_WARPS ? 2 : 1;
     const long long tiles = ((long long)p.T + AP_WARPS * p.tok_warp - 1) / (AP_WARPS * p.tok_warp);
     p.splits = (int)std::max(1LL, std::min((long long)groups, 2 * 152 / tiles));
     p.v_tile = value_tile(p.T, p.kv.n_kv);
