@@ -579,3 +579,115 @@ def test_wrong_tensors_are_refused():
         z.chunk_append(b.pool, 0, torch.zeros(2, 3 * 128, device=DEV), i32([0, 0]), torch.zeros(2, dtype=torch.int32, device=DEV))
     with pytest.raises(z.ZdecError):
         z.chunk_append(b.pool, 0, torch.zeros(2, 3 * 128, device=DEV), i32([0, 0]), torch.zeros(2, dtype=torch.int64, device=DEV))
+
+
+# ------------------------------------- many tokens, many requests, extremes
+@pytest.mark.parametrize("types", PAIRS)
+@pytest.mark.parametrize("order", ["run", "any"])
+def test_append_and_read_of_whole_tiles(types, order):
+    """Enough tokens for CTAs of 64: codes on exact halves, zero blocks, the
+    largest values (a Q8_0 product past fp16's top is read as 65504), runs of
+    slots that start inside a 16-byte segment."""
+    T, n_kv = 1300, 8
+    g = torch.Generator(device=DEV).manual_seed(21)
+    pages = T // 64 + 3
+    pool = _new_pool(pages, 1, n_kv, types)
+    x = (2 * torch.randn(T, 2 * n_kv, 128, generator=g, device=DEV)).half()
+    half = torch.arange(32, device=DEV).half() - 15.5            # amax 127 / 64: scale 2^-6, every other value a tie
+    half[0] = 127.0
+    for at, e in ((7, 0), (64, -6), (700, 3), (T - 1, -12)):
+        x[at, :, 32:64] = half * 2.0 ** e
+        x[at, :, 96:] = -half * 2.0 ** e
+    x[9, :, :64] = 0.0
+    x[640:643, :, 64:96] = 65504.0
+    x[640, :, 70] = -65504.0
+    x[641, :, 0:32] = 6e-8
+    slots = torch.arange(T, device=DEV) + 5 if order == "run" else torch.randperm(pages * 64, generator=g, device=DEV)[:T].contiguous()
+    z.chunk_append(pool, 0, x.flatten(1), i32([0] * T), slots, rope_theta=0.0)
+    k, v = (torch.empty(T, n_kv, 128, dtype=torch.float16, device=DEV) for _ in range(2))
+    for take in (slots, slots.roll(3), torch.where(torch.arange(T, device=DEV) % 37 == 5, -1, slots)):
+        z.chunk_read(pool, 0, take, k, v)
+        rows = x.roll(3, 0) if take[0] == slots[-3] else x
+        for got, kind, src in ((k, types[0], rows[:, :n_kv]), (v, types[1], rows[:, n_kv:])):
+            want = _encode(kind, src).clamp(-65504, 65504).half()
+            same = got == torch.where((take >= 0)[:, None, None], want, 0)
+            assert bool(same.all()), (~same).nonzero()[:5].tolist()
+
+
+def test_append_of_many_tokens_is_that_of_its_parts():
+    """Thousands of tokens (two per warp) against calls of 700: the same bits."""
+    T, n_q, n_kv = 5003, 5, 2
+    g = torch.Generator(device=DEV).manual_seed(22)
+    x = torch.randn(T, (n_q + 2 * n_kv) * 128, generator=g, device=DEV).bfloat16()
+    pos = torch.randint(0, 10 ** 6, (T,), generator=g, device=DEV).int()
+    slots = torch.randperm(T + 70, generator=g, device=DEV)[:T].contiguous()
+    outs = []
+    for step in (T, 700):
+        pool = _new_pool((T + 70) // 64 + 1, 1, n_kv, (1, 2))
+        q = torch.empty(T, n_q, 128, dtype=torch.bfloat16, device=DEV)
+        for a in range(0, T, step):
+            part = slice(a, min(a + step, T))
+            z.chunk_append(pool, 0, x[part], pos[part].contiguous(), slots[part].contiguous(), q[part], rope_theta=1e6)
+        outs.append((q, pool.pages))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("R,n_q,new,types", [(32, 4, 1, (2, 2)), (33, 4, 1, (0, 0)), (512, 2, 1, (1, 1)), (513, 2, 1, (2, 2)), (1100, 2, 1, (0, 0)),
+                                             (520, 16, 9, (0, 0)), (530, 16, 9, (1, 2))])
+def test_attention_of_many_requests(R, n_q, new, types):
+    """Around 32 and 512 requests, where their weights are summed in another
+    way; single tokens (row blocks of 128) and several (of 256)."""
+    lens = [(new + (i * 37) % 150, 1 + (i * 5) % new if i % 3 else new) for i in range(R)]
+    b = Batch(lens, n_q, 1, types, torch.float16, seed=R, layers=1)
+    b.check(b.run())
+
+
+def test_attention_with_a_length_past_the_table():
+    """A kv_len above 64 * max_pages counts as that."""
+    b = Batch([(128, 5), (100, 30)], 4, 1, (0, 0), torch.float16, seed=23)
+    b.tables = b.tables[:, :2].contiguous()
+    want = b.run()
+    b.kv_len[0] = 5000
+    status = i32([0])
+    assert torch.equal(b.run(status=status), want) and status.item() == 0
+    b.kv_len[0] = 2 ** 31 - 1
+    assert torch.equal(b.run(status=status), want) and status.item() == 0
+
+
+def test_attention_of_bf16_queries_of_any_size():
+    """Rows from 2^-130 to 2^120 in one call (the largest brought into fp16's
+    range row by row): small ones weigh their keys evenly, large ones as usual."""
+    b = Batch([(300, 200), (90, 1), (70, 3)], 4, 2, (0, 1), torch.bfloat16, seed=24, spread=1.0)
+    e = torch.tensor([-130, -60, 0, 60, 113, 120], device=DEV)[torch.arange(b.T * 4, device=DEV) % 6].view(b.T, 4, 1)
+    b.q = (b.q.double() * 2.0 ** e).bfloat16()
+    b.q[17] = 0.0
+    b.check(b.run(scale=2.0 ** -120), scale=2.0 ** -120)
+
+
+def test_attention_graphs_that_replay_together():
+    """Two captured calls with their own workspaces, replayed on two streams at
+    the same time, between eager calls on a third."""
+    bs = [Batch([(3000, 1), (800, 1), (64, 1)], 8, 2, (2, 2), torch.bfloat16, seed=25), Batch([(1500, 300), (64, 64)], 8, 2, (0, 0), torch.float16, seed=26)]
+    want = [b.run() for b in bs]
+    torch.cuda.synchronize()
+    streams, graphs, outs = [torch.cuda.Stream() for _ in bs], [], [torch.full_like(b.q, 5.0) for b in bs]
+    for b, s, o in zip(bs, streams, outs):
+        with torch.cuda.stream(s):
+            b.run(o=o)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                b.run(o=o)
+        graphs.append(g)
+    third = Batch([(700, 40)], 4, 1, (1, 1), torch.float16, seed=27)
+    alone = third.run()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for o in outs:
+            o.fill_(1.0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = third.run()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, alone)
