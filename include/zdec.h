@@ -429,6 +429,7 @@ enum { ZDEC_CHUNK_BAD_SLOT = 1,   /* append, read: a slot past the pool (its row
  * and slot -1; tokens past T are not written (nor the table entries that they
  * would set).  A negative length counts as 0.  Lengths and the total stay
  * below 2^31.  Two calls that set entries of the same table must be ordered.
+ * No output may overlap ctx_len or n_new (refused).
  * cu [R+1], kv_len [R], positions [T], slots [T], taken [2]. 0 <= R <= 2^20,
  * 0 <= T < 2^31. */
 zdec_status zdec_chunk_plan(int R, const int32_t *ctx_len_dev, const int32_t *n_new_dev,
@@ -456,7 +457,8 @@ typedef struct {
  * rules of zdec_kv_dtype) at slots_dev[t].  A token with slot -1 (any negative
  * value) writes no K/V, its query is still rotated.  Slots are distinct: of
  * two tokens with one slot, either may be there afterwards, element by
- * element.  status_dev: optional device word (NULL: none). */
+ * element.  q_out may not overlap qkv (refused; other columns of one matrix are
+ * fine).  status_dev: optional device word (NULL: none). */
 zdec_status zdec_chunk_append(const zdec_pool *pool, int layer, const zdec_rope *rope, int T, int n_q,
                               const void *qkv_dev, int in_type, long long qkv_ld,
                               const int32_t *positions_dev, const int64_t *slots_dev,
@@ -464,14 +466,16 @@ zdec_status zdec_chunk_append(const zdec_pool *pool, int layer, const zdec_rope 
 
 /* K and V of T slots of layer `layer` as fp16 rows k_dev, v_dev
  * [T][n_kv_heads][128] (16-byte aligned): fp16 as stored, FP8 exactly, Q8_0 as
- * code * scale rounded to fp16; negative and out-of-range slots read as 0.
+ * code * scale rounded to fp16 (at most 65504 in size); negative and
+ * out-of-range slots read as 0.  k, v and the pool do not overlap.
  * status_dev as above. */
 zdec_status zdec_chunk_read(const zdec_pool *pool, int layer, int T, const int64_t *slots_dev,
                             void *k_dev, void *v_dev, uint32_t *status_dev, void *stream);
 
 /* Attention of the new tokens of R requests over their pages:
  *   o[t][h] = sum_j softmax_j(scale * q[t][h] . k[j][h / (n_q / n_kv)]) v[j][...]
- * over the keys j < kv_len[r] (at most 64 * max_pages) that token t sees:
+ * over the keys j < kv_len[r] (a kv_len above 64 * max_pages counts as that, a
+ * negative one as 0) that token t sees:
  *   causal: j <= kv_len[r] - n + i for the i-th of the request's n tokens (the
  *     new tokens are the last of the kv_len[r] cached ones; with kv_len < n
  *     the first tokens see nothing), and with window > 0 only the last
@@ -481,11 +485,13 @@ zdec_status zdec_chunk_read(const zdec_pool *pool, int layer, int T, const int64
  * does not see have no influence, whatever they hold.  Keys without a page in
  * the pool are left out (ZDEC_CHUNK_NO_PAGE).
  * q_dev, o_dev: fp16 or bf16 (io_type) rows of n_q heads of 128, q_ld and o_ld
- * elements apart (multiples of 8; 16-byte aligned; they may not overlap).
+ * elements apart (multiples of 8; 16-byte aligned).  o may not overlap q
+ * (refused; other columns of one matrix are fine).
  * cu_dev [R+1] with cu[0] = 0, not decreasing; tokens past T are left out and
  * rows behind cu[R] are not touched.  tables_dev [R][max_pages].
  * Scores, softmax statistics and sums are fp32; probabilities enter the
- * second product as fp16, and so do Q8_0 values (code * scale).
+ * second product as fp16, and so do Q8_0 keys and values (code * scale, the
+ * scale at most 515.5 there: a block's largest stays below fp16's top).
  * workspace_dev: zdec_chunk_attention_workspace_bytes(n_q, n_kv) bytes,
  * 256-byte aligned, any content; calls that may overlap in time need their
  * own (two captured graphs that replay together too). */

@@ -2,6 +2,7 @@
 // launches (include/zdec.h, "chunks of new tokens").
 #include <algorithm>
 #include <array>
+#include <initializer_list>
 #include <cmath>
 
 #include "chunk.cuh"
@@ -45,6 +46,16 @@ KvPool kv_of(const zdec_pool *pool, const int32_t *tables, int max_pages) {
     kv.max_pages = max_pages;
     return kv;
 }
+// Whether two arrays, or T rows of wa and wb bytes that are la and lb bytes
+// apart, share a byte.  Columns of one matrix (la == lb) may lie between each
+// other; rows of different strides whose extents meet count as sharing.
+bool overlap(const void *a, long long wa, const void *b, long long wb, long long T = 1, long long la = 0, long long lb = 0) {
+    const __int128 x = (uintptr_t)a, y = (uintptr_t)b, d = y - x, rows = T - 1;
+    if (!a || !b || wa <= 0 || wb <= 0 || x + rows * la + wa <= y || y + rows * lb + wb <= x) return false;
+    if (la != lb || la == 0) return true;
+    const long long in = (long long)(((d % la) + la) % la);   // where b's rows start within a's
+    return in < wa || in + wb > la;
+}
 }  // namespace
 
 extern "C" size_t zdec_page_bytes(int k_type, int v_type, int n_layers, int n_kv_heads) {
@@ -63,6 +74,11 @@ extern "C" zdec_status zdec_chunk_plan(int R, const int32_t *ctx_len_dev, const 
     if (!cu_dev || !taken_dev || (R > 0 && (!ctx_len_dev || !n_new_dev || !tables_dev || !kv_len_dev)) ||
         (T > 0 && (!positions_dev || !slots_dev)))
         return fail_global(ZDEC_ERR_ARG, "null pointer");
+    const long long r4 = 4LL * R;   // every CTA reads all lengths, at any time
+    for (const int32_t *in : {ctx_len_dev, n_new_dev})
+        if (overlap(in, r4, cu_dev, r4 + 4) || overlap(in, r4, kv_len_dev, r4) || overlap(in, r4, taken_dev, 8) ||
+            overlap(in, r4, positions_dev, 4LL * T) || overlap(in, r4, slots_dev, 8LL * T))
+            return fail_global(ZDEC_ERR_ARG, "an output overlaps ctx_len or n_new");
     CK(launch_chunk_plan(R, ctx_len_dev, n_new_dev, free_pages_dev, n_free, tables_dev, max_pages, T, cu_dev, kv_len_dev,
                          positions_dev, slots_dev, taken_dev, (cudaStream_t)stream));
     return ZDEC_OK;
@@ -92,6 +108,9 @@ extern "C" zdec_status zdec_chunk_append(const zdec_pool *pool, int layer, const
         return fail_global(ZDEC_ERR_ARG, "qkv rows must be 16-byte aligned, qkv_ld a multiple of 8 that holds n_q + 2 n_kv heads");
     if (n_q > 0 && (q_ld < (long long)n_q * HD || q_ld % 8 || !aligned16(q_out_dev)))
         return fail_global(ZDEC_ERR_ARG, "q rows must be 16-byte aligned, q_ld a multiple of 8 that holds n_q heads");
+    const long long es = in_type == ZDEC_F32 ? 4 : 2;
+    if (n_q > 0 && overlap(qkv_dev, (n_q + 2LL * pool->n_kv_heads) * HD * es, q_out_dev, 2LL * n_q * HD, T, qkv_ld * es, q_ld * 2))
+        return fail_global(ZDEC_ERR_ARG, "q overlaps qkv");
     ChunkAppendParams p{};
     p.kv = kv_of(pool, nullptr, 0);
     p.layer = layer;
@@ -178,6 +197,7 @@ extern "C" zdec_status zdec_chunk_attention(const zdec_pool *pool, int layer, co
         return fail_global(ZDEC_ERR_ARG, "q and o rows must be 16-byte aligned, their strides multiples of 8 that hold n_q heads");
     if (!workspace_dev || (uintptr_t)workspace_dev % 256) return fail_global(ZDEC_ERR_ARG, "the workspace must be 256-byte aligned");
     if (workspace_bytes < zdec_chunk_attention_workspace_bytes(a->n_q, nkv)) return fail_global(ZDEC_ERR_ARG, "workspace too small");
+    if (overlap(q_dev, need * 2, o_dev, need * 2, a->T, a->q_ld * 2, a->o_ld * 2)) return fail_global(ZDEC_ERR_ARG, "o overlaps q");
     ChunkAttnParams p{};
     p.kv = kv_of(pool, tables_dev, a->max_pages);
     p.layer = layer;

@@ -122,3 +122,20 @@ def test_host_tensors_are_refused():
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(z.ZdecError, match="CUDA tensor"):
         z.chunk_plan(i, i, i[None], torch.zeros(2, dtype=torch.int32), i, i, i.long(), torch.zeros(2, dtype=torch.int32))
+
+
+def test_overlapping_arrays_are_refused():
+    lib, at = z.load_library(), lambda x: ctypes.c_void_p(1 << 20 | x)
+    c = dict(R=100, ctx=at(0), new=at(4096), free=None, n_free=0, tables=at(8192), max_pages=2, T=10, cu=at(16384), kv_len=at(20480), pos=at(24576),
+             slots=at(28672), taken=at(32768))
+    for out, where in (("kv_len", 0), ("kv_len", 396), ("cu", 4096 + 8), ("taken", 4096 + 392), ("pos", 4096 - 4), ("slots", 392)):
+        assert lib.zdec_chunk_plan(*{**c, out: at(where)}.values(), None) == -1 and "overlaps" in _msg(), (out, where)
+    pool, rope = _pool(), z._Rope(1e6, 1, (ctypes.c_int * 4)(64))
+    # (in type, ld, q, q_ld): in place; from the middle; the key columns of the same matrix; another stride
+    for typ, ld, q, q_ld in ((1, 1024, 0, 1024), (1, 1024, 512, 1024), (1, 1024, 2 * 512, 1024), (0, 1024, 4 * 1000, 2048), (1, 2048, 2 * 2048 - 16, 512)):
+        assert lib.zdec_chunk_append(ctypes.byref(pool), 0, ctypes.byref(rope), 7, 4, at(0), typ, ld, P16, P16, at(q), 1, q_ld, None, None) == -1
+        assert "q overlaps qkv" in _msg(), (typ, ld, q, q_ld)
+    for q_ld, o, o_ld in ((512, 0, 512), (1024, 1008, 1024), (1024, 2048 - 16, 1024), (1024, 1024, 512)):
+        a = z._ChunkAttn(4, 1, 7, 1, 1, 1, 0, 0.1, q_ld, o_ld)
+        assert lib.zdec_chunk_attention(ctypes.byref(pool), 0, ctypes.byref(a), P16, P16, P16, at(0), at(o), P16, 1 << 30, None, None) == -1
+        assert "o overlaps q" in _msg(), (q_ld, o, o_ld)

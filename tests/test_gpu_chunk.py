@@ -691,3 +691,19 @@ def test_attention_graphs_that_replay_together():
         eager = third.run()
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, alone)
+
+
+def test_queries_and_outputs_as_columns_of_one_matrix():
+    """qkv, rotated queries and attention outputs side by side: allowed, and
+    the same bits as with arrays of their own."""
+    b = Batch([(100, 37), (70, 5)], 4, 2, (0, 0), torch.float16, seed=28)
+    n = 4 * 128
+    wide = torch.full((b.T, 8 * 128 + 2 * n), 3.0, dtype=torch.float16, device=DEV)
+    wide[:, :8 * 128] = torch.randn(b.T, 8 * 128, device=DEV)
+    pos, none = i32(range(b.T)), torch.full((b.T,), -1, dtype=torch.int64, device=DEV)
+    q, o = wide[:, 8 * 128:8 * 128 + n].unflatten(1, (4, 128)), wide[:, 8 * 128 + n:].unflatten(1, (4, 128))
+    z.chunk_append(b.pool, b.layer, wide[:, :8 * 128], pos, none, q, rope_theta=1e4)
+    b.run(q=q, o=o)
+    own = torch.empty(b.T, 4, 128, dtype=torch.float16, device=DEV)
+    z.chunk_append(b.pool, b.layer, wide[:, :8 * 128].contiguous(), pos, none, own, rope_theta=1e4)
+    assert torch.equal(q, own) and torch.equal(o, b.run(q=own))
