@@ -29,6 +29,24 @@
 //
 // Items cut between CTAs leave (m, l, O) in the workspace; a second kernel
 // joins them in key order, so the result does not depend on timing.
+//
+// What bounds it (GB300, graph replays, both kernels):
+// - 2048 tokens behind 30000 cached ones, fp16, 32 query and 8 kv heads: 700 us,
+//   1490 TFLOP/s (77 % of cuBLAS's burst bf16 rate).  A chunk of two tiles takes
+//   about 3300 cycles: its 32 MMAs 2048 of them, the softmax of its 256 rows on the
+//   other side 1024 for the exp2 alone (4 cycles per warp and SM quarter) beside
+//   packed fp32 arithmetic and TMEM reads; the two overlap, hand-overs do not.
+// - the same from an FP8 cache: 850 us.  Eight bytes of a raw page become
+//   sixteen, in and out of shared memory, on four warps with 96 registers; they
+//   need as long as the softmax.  More warps would take the softmax's registers.
+// - a step of 8 sequences, 800 to 30000 tokens, Q8_0: 76 us where the bytes
+//   take 24; the conversion again, and 4 us of start, 5 us of joining.
+// - one token over 2048, fp16: 14.7 us: launches, the walk to the first chunk, one
+//   chunk, the epilogue and the join, each a microsecond or two of latency.
+// Not kept, all slower: the conversions rolled up or further unrolled, K and V on
+// warps of their own, the softmax of 256 quantised rows in two passes over S, one
+// rolled loop for both buffers' MMAs, waiting for P V before the next Q K^T (the
+// tensor core runs them in the order of issue).
 #include <cuda.h>
 
 #include <atomic>
@@ -364,53 +382,85 @@ __device__ __forceinline__ float v_at(const uint8_t *slot, int j, int d) {
                                                           ((((j & 31) >> 3) ^ ((d >> 1) & 3)) << 4) + (j & 7) * 2));
 }
 
-// The 32 rows of a warp into its part of a Q operand tile, two rows of 16
-// lanes x 16 bytes at a time (`src`: this lane's row), all loads in flight
-// together.  fp16 as it is; a bf16 row times 2^-e, which brings its largest
-// element below fp16's top (exact but for elements below 2^-28 of it): in
-// place afterwards.  Returns e of this lane's row.  Rows from n_rows on stay as
+// The 32 rows of a warp into its part of a Q operand tile (`src`: this lane's
+// row), copied two rows of 16 lanes x 16 bytes at a time, BATCH of them in
+// flight (8 for the prompts of one-byte caches: 2048 tokens over 6000 FP8 keys
+// 251 to 238 us; 4 else: over fp16 ones 189 and 191, a step of 8 76 and 78).  fp16 stays as it
+// is.  A bf16 row is multiplied in place by 2^-e, which brings its largest
+// element below fp16's top (exact but for elements below 2^-28 of it): by the
+// lane that owns it (sixteen conflict-free 16-byte accesses, no exchange between
+// lanes: prompts of a mixed batch 120 to 114 us), or where warps hold FEW rows by
+// the 16 lanes that copied it (a step of 8: 77 us, with the other form 83).
+// Returns e of this lane's row.  Rows from n_rows on stay as
 // they are: a row of the MMA touches no other.
+template <bool FEW, int BATCH>
 __device__ __forceinline__ int load_q(const uint16_t *src, int io_type, bool store, uint8_t *tile, int row0, int n_rows) {
     const int lane = threadIdx.x & 31, c = lane & 15, up = lane >> 4;
     uint8_t *to = tile + (c >> 3) * 16384 + (row0 + up) * 128;
     if (store) {
 #pragma unroll 1
-        for (int i0 = 0; 2 * i0 < n_rows; i0 += 4) {
-            uint4 v[4];
+        for (int i0 = 0; 2 * i0 < n_rows; i0 += BATCH) {
+            uint4 v[BATCH];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < BATCH; i++) {
                 const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * (i0 + i) + up);
                 v[i] = __ldg(reinterpret_cast<const uint4 *>(from) + c);
             }
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int i = 0; i < BATCH; i++)
                 *reinterpret_cast<uint4 *>(to + (i0 + i) * 256 + (((c ^ (2 * (i0 + i) + up)) & 7) << 4)) = v[i];
         }
     }
     if (io_type == ZDEC_F16) return 0;
-    int mine = 0;
+    __syncwarp();
+    if (FEW) {
+        int mine = 0;
 #pragma unroll 1
-    for (int i = 0; 2 * i < n_rows; i++) {
-        uint4 *at = reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4));
-        const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * i + up);
-        const uint4 x = store ? *at : __ldg(reinterpret_cast<const uint4 *>(from) + c);
-        uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;   // largest magnitude bits of the row
+        for (int i = 0; 2 * i < n_rows; i++) {
+            uint4 *at = reinterpret_cast<uint4 *>(to + i * 256 + (((c ^ (2 * i + up)) & 7) << 4));
+            const uint16_t *from = (const uint16_t *)__shfl_sync(CAF, (unsigned long long)src, 2 * i + up);
+            const uint4 x = store ? *at : __ldg(reinterpret_cast<const uint4 *>(from) + c);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;   // largest magnitude bits of the row
 #pragma unroll
-        for (int k = 0; k < 4; k++) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+            for (int k = 0; k < 4; k++) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(CAF, top, o));
-        const int ex = (int)(top >> 7);                  // biased exponent
-        const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
-        const int both = __shfl_sync(CAF, e, (lane & 1) * 16);
-        if ((lane >> 1) == i) mine = both;
-        // 2^-e, e in [-140, 113]: 2^140 in two steps
-        const float f1 = __int_as_float((127 + min(-e, 100)) << 23), f2 = __int_as_float((127 + max(-e - 100, 0)) << 23);
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(CAF, top, o));
+            const int ex = (int)(top >> 7);                  // biased exponent
+            const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
+            const int both = __shfl_sync(CAF, e, (lane & 1) * 16);
+            if ((lane >> 1) == i) mine = both;
+            // 2^-e, e in [-140, 113]: 2^140 in two steps
+            const float f1 = __int_as_float((127 + min(-e, 100)) << 23), f2 = __int_as_float((127 + max(-e - 100, 0)) << 23);
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            w[k] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2));
-        if (store) *at = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 4; k++)
+                w[k] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2));
+            if (store) *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return mine;
     }
-    return mine;
+    uint8_t *row = tile + (row0 + lane) * 128;
+    auto at = [&](int k) { return reinterpret_cast<uint4 *>(row + (k >> 3) * 16384 + (((k ^ lane) & 7) << 4)); };
+    uint32_t top2 = 0;                                   // largest magnitude bits, of even and odd elements
+#pragma unroll 4
+    for (int k = 0; k < 16; k++) {
+        const uint4 x = store ? *at(k) : __ldg(reinterpret_cast<const uint4 *>(src) + k);
+        top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+    }
+    const int ex = (int)(max(top2 & 0xFFFFu, top2 >> 16) >> 7);   // biased exponent
+    const int e = ex == 0 || ex == 255 ? 0 : ex - 127 - 14;
+    if (!store) return e;
+    // 2^-e, e in [-140, 113]: 2^140 in two steps
+    const float f1 = __int_as_float((127 + min(-e, 100)) << 23), f2 = __int_as_float((127 + max(-e - 100, 0)) << 23);
+#pragma unroll 4
+    for (int k = 0; k < 16; k++) {
+        const uint4 x = *at(k);
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            w[i] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2));
+        *at(k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return e;
 }
 // 256 bytes of each of a warp's 32 rows, staged in shared memory in the same
 // arrangement, to `dst` (this lane's row; null: not written).
@@ -619,200 +669,200 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
 
     // registers: 4 warpgroups x 128 at launch = 64 + 80 + 2 x 184, or 64 + 96 + 2 x 176; short items need no other split
     if (group == 0) {
-    if (ROWS > 128) reg_dec<64>();
-    if (warp == 0) {
-        // ---------------------------------------------------------- copies ---
-        const uint32_t kb = kv_region_bytes(p.kv.k_type), vb = kv_region_bytes(p.kv.v_type);
-        const size_t coff = kv_chunk_off(p.kv, p.layer, 0);
-        uint32_t it = 0, dir = 0, raw = 0, ci = 0;   // operands, those landing as such, raw pages; chunks
-        bool ok = true;
-        for (; ok && next(); done()) {
-            const Segment s = sh.seg[si % CA_SEGS];
-            const bool two = ROWS > 128 && s.rows > 128;
-            const int32_t *row = p.kv.table + (size_t)s.r * p.kv.max_pages;
-            const size_t off = coff + (size_t)s.h * (kb + vb);
-            // pages of 16 chunks, one per lane; V lags K by up to two chunks, so the 16 before are kept
-            auto pages_of = [&](int c16) {
-                const long long pg = ((long long)s.c0 + 16 * c16) * 2 + lane;
-                return pg < p.kv.max_pages && pg * 64 < s.kv ? __ldg(row + pg) : -2;   // -2: no key there
-            };
-            int now = pages_of(0), before = -2, now_i = 0;
-            for (int i = 0; ok && i < 2 * s.n_c; i++, it++) {
-                int kv, c;
-                item_at(i, s.n_c, two, kv, c);
-                if (kv == 0 && (c >> 4) != now_i) {
-                    before = now;
-                    now_i = c >> 4;
-                    now = pages_of(now_i);
-                }
-                const int from = (c >> 4) == now_i ? now : before;
-                const int pa = __shfl_sync(CAF, from, 2 * (c & 15)), pb = __shfl_sync(CAF, from, 2 * (c & 15) + 1);
-                const int okm = (kv_page_ok(p.kv, pa) ? 1 : 0) | (kv_page_ok(p.kv, pb) ? 2 : 0);
-                if (lane == 0) {
-                    const uint32_t bytes = kv ? vb : kb;
-                    const size_t at = off + (kv ? kb : 0);
-                    if (kv ? v16 : k16) {
-                        const uint32_t sl = it % NS;
-                        ok = it < NS || wait(&sh.empty[sl], (it / NS - 1) & 1);
-                        if (ok) {
-                            // chunk ci + c's entry was last read for chunk ci + c - 8, whose operands have left their slots
-                            if (kv == 0) sh.pages_ok[(ci + c) & 7] = okm;
-                            uint8_t *dst = slots + sl * CA_SLOT;
-                            uint64_t *bar = &sh.full[dir % CA_MAX_SLOTS];
-                            dir++;
-                            if (okm) mbar_expect_tx(bar, __popc(okm) * bytes);
-                            else mbar_arrive1(bar);
-#pragma unroll 1
-                            for (int k = 0; k < 2; k++) {
-                                if (!((okm >> k) & 1)) continue;
-                                const int page = k ? pb : pa;
-                                if (kv) bulk_g2s(dst + k * 16384, p.kv.base + (size_t)page * p.kv.page_bytes + at, bytes, bar);
-                                else
-                                    for (int half = 0; half < 2; half++)
-                                        tma_k_half(dst + half * 16384 + k * 8192, &k_map, half, p.layer * n_kv + s.h, page, bar);
-                            }
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; ok && k < 2; k++) {
-                            const uint32_t sl = raw % NR;
-                            ok = raw < NR || wait(&sh.raw_empty[sl], (raw / NR - 1) & 1);
-                            if (!ok) break;
-                            if (kv == 0 && k == 0) sh.pages_ok[(ci + c) & 7] = okm;
-                            uint64_t *bar = &sh.raw_full[sl];
-                            raw++;
-                            if ((okm >> k) & 1) {
-                                mbar_expect_tx(bar, bytes);
-                                bulk_g2s(raws + sl * CA_RAW, p.kv.base + (size_t)(k ? pb : pa) * p.kv.page_bytes + at, bytes, bar);
-                            } else {
-                                mbar_arrive1(bar);
-                            }
-                        }
-                    }
-                    if (p.status && kv == 0 && ((!(okm & 1) && pa != -2) || (!(okm & 2) && pb != -2)))
-                        atomicOr(p.status, (uint32_t)ZDEC_CHUNK_NO_PAGE);
-                }
-                ok = __shfl_sync(CAF, (int)ok, 0);
-            }
-            ci += s.n_c;
-        }
-        // copies in flight land before the CTA leaves, also where a wait gave up
-        if (lane == 0 && sh.abort) {
-            const uint32_t t0 = (uint32_t)clock();
-            for (uint32_t i = dir > CA_MAX_SLOTS ? dir - CA_MAX_SLOTS : 0; i < dir; i++)
-                while (!mbar_try_wait(&sh.full[i % CA_MAX_SLOTS], (i / CA_MAX_SLOTS) & 1) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
-            for (uint32_t i = raw > NR ? raw - NR : 0; !ALL_F16 && i < raw; i++)
-                while (!mbar_try_wait(&sh.raw_full[i % NR], (i / NR) & 1) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
-        }
-    } else if (warp == 1) {
-        // -------------------------------------------------------------- MMA ---
-        if (elect_one()) {
-            constexpr uint32_t IDESC = MMA_IDESC_F16<128, 128>;
-            const uint64_t q_desc = mma_desc_sw128(smem_u32(q_smem)), k_desc = mma_desc_sw128(smem_u32(slots)),
-                           v_desc = mma_desc_sw64(smem_u32(slots));
-            uint32_t it0 = 0, ci = 0, segs[2] = {0, 0}, n_p[2] = {0, 0};   // operands, chunks before; segments, steps per buffer
+        if (ROWS > 128) reg_dec<64>();
+        if (warp == 0) {
+            // ---------------------------------------------------------- copies ---
+            const uint32_t kb = kv_region_bytes(p.kv.k_type), vb = kv_region_bytes(p.kv.v_type);
+            const size_t coff = kv_chunk_off(p.kv, p.layer, 0);
+            uint32_t it = 0, dir = 0, raw = 0, ci = 0;   // operands, those landing as such, raw pages; chunks
             bool ok = true;
-            auto ready = [&](uint32_t item) { return wait(&sh.ready[item % NS], (item / NS) & 1); };
-            for (; ok; si++) {
-                ok = wait(&sh.seg_full[si % CA_SEGS], (si / CA_SEGS) & 1);
-                const int n_c = sh.seg[si % CA_SEGS].n_c;
-                const bool two = ROWS > 128 && sh.seg[si % CA_SEGS].rows > 128;
-                if (!ok || n_c < 0) break;
-                mbar_arrive1(&sh.seg_empty[si % CA_SEGS]);
-                if (n_c == 0) continue;
-                const int steps = two ? 2 * n_c : n_c;
-                for (int t = 0; t < (two ? 2 : 1); t++) ok = ok && wait(&sh.q_ready[t], segs[t]++ & 1);
-                // step i: chunk i / 2 of tile i % 2, or chunk i of the one tile, in buffer i % 2; its S two steps ahead
+            for (; ok && next(); done()) {
+                const Segment s = sh.seg[si % CA_SEGS];
+                const bool two = ROWS > 128 && s.rows > 128;
+                const int32_t *row = p.kv.table + (size_t)s.r * p.kv.max_pages;
+                const size_t off = coff + (size_t)s.h * (kb + vb);
+                // pages of 16 chunks, one per lane; V lags K by up to two chunks, so the 16 before are kept
+                auto pages_of = [&](int c16) {
+                    const long long pg = ((long long)s.c0 + 16 * c16) * 2 + lane;
+                    return pg < p.kv.max_pages && pg * 64 < s.kv ? __ldg(row + pg) : -2;   // -2: no key there
+                };
+                int now = pages_of(0), before = -2, now_i = 0;
+                for (int i = 0; ok && i < 2 * s.n_c; i++, it++) {
+                    int kv, c;
+                    item_at(i, s.n_c, two, kv, c);
+                    if (kv == 0 && (c >> 4) != now_i) {
+                        before = now;
+                        now_i = c >> 4;
+                        now = pages_of(now_i);
+                    }
+                    const int from = (c >> 4) == now_i ? now : before;
+                    const int pa = __shfl_sync(CAF, from, 2 * (c & 15)), pb = __shfl_sync(CAF, from, 2 * (c & 15) + 1);
+                    const int okm = (kv_page_ok(p.kv, pa) ? 1 : 0) | (kv_page_ok(p.kv, pb) ? 2 : 0);
+                    if (lane == 0) {
+                        const uint32_t bytes = kv ? vb : kb;
+                        const size_t at = off + (kv ? kb : 0);
+                        if (kv ? v16 : k16) {
+                            const uint32_t sl = it % NS;
+                            ok = it < NS || wait(&sh.empty[sl], (it / NS - 1) & 1);
+                            if (ok) {
+                                // chunk ci + c's entry was last read for chunk ci + c - 8, whose operands have left their slots
+                                if (kv == 0) sh.pages_ok[(ci + c) & 7] = okm;
+                                uint8_t *dst = slots + sl * CA_SLOT;
+                                uint64_t *bar = &sh.full[dir % CA_MAX_SLOTS];
+                                dir++;
+                                if (okm) mbar_expect_tx(bar, __popc(okm) * bytes);
+                                else mbar_arrive1(bar);
 #pragma unroll 1
-                for (int i = -2; i < steps; i++) {
-                    const int u = i & 1;
-                    if (i >= 0) {
-                        const int c = two ? i >> 1 : i;
-                        const uint32_t item = it0 + v_item(c, n_c, two);
-                        if (!two || u == 0) ok = ok && ready(item);
-                        ok = ok && wait(&sh.p_ready[u][0], n_p[u] & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = v_desc + (item % NS) * (CA_SLOT >> 4);
-                        const uint32_t od = tmem + 256 + u * 128;
-                        // a chunk whose product the softmax threads make themselves only reports
-                        const bool bad = sh.bad[(ci + c) & 7] != 0;
-                        if (!bad)
-#pragma unroll
-                            for (int k = 0; k < 4; k++)    // keys 0-63
-                                mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, i > 1 || k > 0);
-                        ok = wait(&sh.p_ready[u][1], n_p[u] & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (!bad)
-#pragma unroll
-                            for (int k = 4; k < 8; k++)
-                                mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, true);
-                        mma_commit(&sh.o_done[u]);
-                        if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
-                        n_p[u]++;
-                    }
-                    if (i + 2 < steps) {
-                        const uint32_t item = it0 + k_item(two ? (i + 2) >> 1 : i + 2, two);
-                        if (!two || u == 0) ok = ok && ready(item);
-                        if (!ok) break;
-                        tc_fence_after();
-                        tc_fence_order();   // S overwrites the P that the PV before reads
-                        const uint64_t qd = q_desc + (two ? u * (32768 >> 4) : 0), kd = k_desc + (item % NS) * (CA_SLOT >> 4);
-#pragma unroll
-                        for (int k = 0; k < 8; k++) {
-                            const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                            mma_ss(tmem + u * 128, qd + o, kd + o, IDESC, k > 0);
+                                for (int k = 0; k < 2; k++) {
+                                    if (!((okm >> k) & 1)) continue;
+                                    const int page = k ? pb : pa;
+                                    if (kv) bulk_g2s(dst + k * 16384, p.kv.base + (size_t)page * p.kv.page_bytes + at, bytes, bar);
+                                    else
+                                        for (int half = 0; half < 2; half++)
+                                            tma_k_half(dst + half * 16384 + k * 8192, &k_map, half, p.layer * n_kv + s.h, page, bar);
+                                }
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; ok && k < 2; k++) {
+                                const uint32_t sl = raw % NR;
+                                ok = raw < NR || wait(&sh.raw_empty[sl], (raw / NR - 1) & 1);
+                                if (!ok) break;
+                                if (kv == 0 && k == 0) sh.pages_ok[(ci + c) & 7] = okm;
+                                uint64_t *bar = &sh.raw_full[sl];
+                                raw++;
+                                if ((okm >> k) & 1) {
+                                    mbar_expect_tx(bar, bytes);
+                                    bulk_g2s(raws + sl * CA_RAW, p.kv.base + (size_t)(k ? pb : pa) * p.kv.page_bytes + at, bytes, bar);
+                                } else {
+                                    mbar_arrive1(bar);
+                                }
+                            }
                         }
-                        mma_commit(&sh.s_full[u]);
-                        if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                        if (p.status && kv == 0 && ((!(okm & 1) && pa != -2) || (!(okm & 2) && pb != -2)))
+                            atomicOr(p.status, (uint32_t)ZDEC_CHUNK_NO_PAGE);
                     }
+                    ok = __shfl_sync(CAF, (int)ok, 0);
                 }
-                it0 += 2 * n_c;
-                ci += n_c;
+                ci += s.n_c;
             }
-            if (!ok) {   // a wait gave up: MMAs in flight end before the CTA leaves
-                mma_commit(&sh.drain);
+            // copies in flight land before the CTA leaves, also where a wait gave up
+            if (lane == 0 && sh.abort) {
                 const uint32_t t0 = (uint32_t)clock();
-                while (!mbar_try_wait(&sh.drain, 0) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
+                for (uint32_t i = dir > CA_MAX_SLOTS ? dir - CA_MAX_SLOTS : 0; i < dir; i++)
+                    while (!mbar_try_wait(&sh.full[i % CA_MAX_SLOTS], (i / CA_MAX_SLOTS) & 1) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
+                for (uint32_t i = raw > NR ? raw - NR : 0; !ALL_F16 && i < raw; i++)
+                    while (!mbar_try_wait(&sh.raw_full[i % NR], (i / NR) & 1) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------------------------- MMA ---
+            if (elect_one()) {
+                constexpr uint32_t IDESC = MMA_IDESC_F16<128, 128>;
+                const uint64_t q_desc = mma_desc_sw128(smem_u32(q_smem)), k_desc = mma_desc_sw128(smem_u32(slots)),
+                               v_desc = mma_desc_sw64(smem_u32(slots));
+                uint32_t it0 = 0, ci = 0, segs[2] = {0, 0}, n_p[2] = {0, 0};   // operands, chunks before; segments, steps per buffer
+                bool ok = true;
+                auto ready = [&](uint32_t item) { return wait(&sh.ready[item % NS], (item / NS) & 1); };
+                for (; ok; si++) {
+                    ok = wait(&sh.seg_full[si % CA_SEGS], (si / CA_SEGS) & 1);
+                    const int n_c = sh.seg[si % CA_SEGS].n_c;
+                    const bool two = ROWS > 128 && sh.seg[si % CA_SEGS].rows > 128;
+                    if (!ok || n_c < 0) break;
+                    mbar_arrive1(&sh.seg_empty[si % CA_SEGS]);
+                    if (n_c == 0) continue;
+                    const int steps = two ? 2 * n_c : n_c;
+                    for (int t = 0; t < (two ? 2 : 1); t++) ok = ok && wait(&sh.q_ready[t], segs[t]++ & 1);
+                    // step i: chunk i / 2 of tile i % 2, or chunk i of the one tile, in buffer i % 2; its S two steps ahead
+#pragma unroll 1
+                    for (int i = -2; i < steps; i++) {
+                        const int u = i & 1;
+                        if (i >= 0) {
+                            const int c = two ? i >> 1 : i;
+                            const uint32_t item = it0 + v_item(c, n_c, two);
+                            if (!two || u == 0) ok = ok && ready(item);
+                            ok = ok && wait(&sh.p_ready[u][0], n_p[u] & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t vd = v_desc + (item % NS) * (CA_SLOT >> 4);
+                            const uint32_t od = tmem + 256 + u * 128;
+                            // a chunk whose product the softmax threads make themselves only reports
+                            const bool bad = sh.bad[(ci + c) & 7] != 0;
+                            if (!bad)
+#pragma unroll
+                                for (int k = 0; k < 4; k++)    // keys 0-63
+                                    mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, i > 1 || k > 0);
+                            ok = wait(&sh.p_ready[u][1], n_p[u] & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (!bad)
+#pragma unroll
+                                for (int k = 4; k < 8; k++)
+                                    mma_ts(od, tmem + u * 128 + k * 8, vd + (((k >> 1) * 8192 + (k & 1) * 32) >> 4), IDESC, true);
+                            mma_commit(&sh.o_done[u]);
+                            if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                            n_p[u]++;
+                        }
+                        if (i + 2 < steps) {
+                            const uint32_t item = it0 + k_item(two ? (i + 2) >> 1 : i + 2, two);
+                            if (!two || u == 0) ok = ok && ready(item);
+                            if (!ok) break;
+                            tc_fence_after();
+                            tc_fence_order();   // S overwrites the P that the PV before reads
+                            const uint64_t qd = q_desc + (two ? u * (32768 >> 4) : 0), kd = k_desc + (item % NS) * (CA_SLOT >> 4);
+#pragma unroll
+                            for (int k = 0; k < 8; k++) {
+                                const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                                mma_ss(tmem + u * 128, qd + o, kd + o, IDESC, k > 0);
+                            }
+                            mma_commit(&sh.s_full[u]);
+                            if (!two || u == 1) mma_commit(&sh.empty[item % NS]);
+                        }
+                    }
+                    it0 += 2 * n_c;
+                    ci += n_c;
+                }
+                if (!ok) {   // a wait gave up: MMAs in flight end before the CTA leaves
+                    mma_commit(&sh.drain);
+                    const uint32_t t0 = (uint32_t)clock();
+                    while (!mbar_try_wait(&sh.drain, 0) && (uint32_t)clock() - t0 < CA_WAIT_LIMIT) {}
+                }
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // --------------------------------------------------------- the walk ---
+            Walk w;
+            w.r = sh.w_r;
+            w.q = sh.w_q;
+            w.J = w.q.blocks();
+            {
+                const long long x = sh.w_x, per = sh.w_per;
+                w.h = (int)div_any(x, per);
+                const long long y = x - w.h * per;
+                int a = 0, b = w.J;   // the block that holds unit y: 32 lanes try as many places at once
+                while (b - a > 1) {
+                    const int step = (b - a + 31) / 32, at = a + lane * step;
+                    const unsigned le = __ballot_sync(CAF, at < b && w.q.before(at) + (long long)ov * at <= y);
+                    const int k = 31 - __clz(le);   // lane 0 always holds
+                    a += k * step;
+                    b = min(b, a + step);
+                }
+                w.j = a;
+                w.off = (int)(y - (a > 0 ? w.q.before(a) + (long long)ov * a : 0));
+                w.ov = ov;
+                w.left = u1 - u0;
+            }
+            if (lane == 0) {
+                bool more = true;
+                for (uint32_t i = 0; more; i++) {
+                    Segment s;
+                    more = next_segment(p, w, u1, W, P, s);
+                    if (!more) s.n_c = -1;
+                    if (i >= CA_SEGS && !wait(&sh.seg_empty[i % CA_SEGS], (i / CA_SEGS - 1) & 1)) break;
+                    sh.seg[i % CA_SEGS] = s;
+                    mbar_arrive1(&sh.seg_full[i % CA_SEGS]);
+                }
             }
         }
-        __syncwarp();
-    } else if (warp == 2) {
-        // --------------------------------------------------------- the walk ---
-        Walk w;
-        w.r = sh.w_r;
-        w.q = sh.w_q;
-        w.J = w.q.blocks();
-        {
-            const long long x = sh.w_x, per = sh.w_per;
-            w.h = (int)div_any(x, per);
-            const long long y = x - w.h * per;
-            int a = 0, b = w.J;   // the block that holds unit y: 32 lanes try as many places at once
-            while (b - a > 1) {
-                const int step = (b - a + 31) / 32, at = a + lane * step;
-                const unsigned le = __ballot_sync(CAF, at < b && w.q.before(at) + (long long)ov * at <= y);
-                const int k = 31 - __clz(le);   // lane 0 always holds
-                a += k * step;
-                b = min(b, a + step);
-            }
-            w.j = a;
-            w.off = (int)(y - (a > 0 ? w.q.before(a) + (long long)ov * a : 0));
-            w.ov = ov;
-            w.left = u1 - u0;
-        }
-        if (lane == 0) {
-            bool more = true;
-            for (uint32_t i = 0; more; i++) {
-                Segment s;
-                more = next_segment(p, w, u1, W, P, s);
-                if (!more) s.n_c = -1;
-                if (i >= CA_SEGS && !wait(&sh.seg_empty[i % CA_SEGS], (i / CA_SEGS - 1) & 1)) break;
-                sh.seg[i % CA_SEGS] = s;
-                mbar_arrive1(&sh.seg_full[i % CA_SEGS]);
-            }
-        }
-    }
     } else if (group == 3) {
         // ------------------------------------------------------- preparing ---
         if (ROWS > 128) reg_dec<ALL_F16 ? 80 : 96>();
@@ -906,7 +956,7 @@ __global__ __launch_bounds__(CA_THREADS, 1) void chunk_attention_kernel(const __
             if (act) {
                 const uint16_t *src = p.q + (long long)(s.t0 + tok) * p.q_ld + (long long)head * HD;
                 const bool mine = two || u == 0;
-                const int e = mine || p.io_type != ZDEC_F16 ? load_q(src, p.io_type, mine, q_smem + first * 256, w4 * 32, min(32, rows - first - w4 * 32)) : 0;
+                const int e = mine || p.io_type != ZDEC_F16 ? load_q<ROWS == 128, (ROWS > 128 && !ALL_F16) ? 8 : 4>(src, p.io_type, mine, q_smem + first * 256, w4 * 32, min(32, rows - first - w4 * 32)) : 0;
                 scale = fmaxf(ldexpf(p.scale_log2, e), 7.9e-31f);   // never 0 (0 * -inf)
             }
             if (two || u == 0) {
