@@ -657,7 +657,7 @@ def chunk_append(cache: KVPool, layer: int, qkv, positions, slots, q_out=None, r
     positions [axes, T] or [T] int32, slots [T] int64 (negative: no K/V),
     q_out [T, n_q, 128] fp16 or bf16 (or None: qkv holds no queries); sections:
     rotary pairs per position axis (sum 64); rope_theta 0: no rotation;
-    status: optional int32 [1].  Asynchronous."""
+    status: optional int32 [1].  q_out may not overlap qkv.  Asynchronous."""
     dt, dev, nkv, axes = _DT or _dtypes(), cache.device, cache.n_kv_heads, len(sections)
     rope = _rope(float(rope_theta), tuple(sections))
     idx = cache.index
@@ -712,7 +712,8 @@ def chunk_attention(cache: KVPool, layer: int, q, o, cu, kv_len, tables, workspa
     (zdec_chunk_attention).  q, o [T, n_q, 128] fp16 or bf16 (rows may be
     strided), int32 cu [R + 1], kv_len [R], tables [R, max_pages]; workspace:
     uint8 CUDA tensor of chunk_attention_workspace_bytes(n_q, n_kv) bytes, one
-    per stream of calls; scale: 1 / sqrt(128) if None.  Asynchronous."""
+    per stream of calls; scale: 1 / sqrt(128) if None.  o may not overlap q.
+    Asynchronous."""
     dt, dev = _DT or _dtypes(), cache.device
     idx, i32 = cache.index, dt["int32"]
     quick = False
